@@ -16,6 +16,8 @@
 #include <cudaTypedefs.h>
 
 #include "attn_mha.cuh"
+#include "attn_ragged.cuh"
+#include "attn_ragged_simt.cuh"
 #include "attn_simt.cuh"
 #include "attn_tc.cuh"
 #include "common.cuh"
@@ -23,7 +25,9 @@
 #include "gemm.cuh"
 #include "gemm_tc.cuh"
 #include "prep.cuh"
+#include "ragged_sched.cuh"
 #include "sched.cuh"
+#include "step.cuh"
 
 using namespace mla;
 
@@ -1260,3 +1264,5 @@ extern "C" mla_status mla_append_latent_noalloc(const mla_weights* w, const void
   return append_noalloc_impl<float>(w, h, seq_idx, pos, page_table, num_seqs, max_pages, num_pages, cache, T,
                                     device_error, scratch, stream);
 }
+
+#include "ragged_api.cuh"

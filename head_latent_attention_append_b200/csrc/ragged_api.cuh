@@ -1,0 +1,287 @@
+// Host side of the ragged-step entry points (include/mla.h): argument checks,
+// workspace layout and launches.  Part of mla_api.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+// Workers of the ragged attention: CTA pairs on the tensor cores, CTAs on the
+// CUDA cores.  The caps size the partial slots.
+constexpr int kRaggedPairs = 80, kRaggedCtas = 160;
+static_assert(kRaggedPairs <= 160 && kRaggedCtas <= 160, "ragged_combine_kernel lists a piece per worker");
+// What changing query rows costs a worker, in tiles of 64 keys: the next rows'
+// load and this block's output (about 6 us against 0.9 us a tile on the tensor
+// cores; small against a tile on the CUDA cores).
+constexpr int kBlockTilesTc = 6, kBlockTilesSimt = 1;
+
+struct RaggedPlan {
+  size_t hdr, vs, pc, worker_seg, segs, split, part_o, part_ml, total;
+  int rows, cap, r_max;
+};
+RaggedPlan make_ragged_plan(const mla_dims& d, int B, int T) {
+  RaggedPlan P{};
+  const bool tc = d.dtype == MLA_BF16;
+  P.rows = tc ? ragged_tc::ROWS : ragged_simt::ROWS;
+  P.cap = tc ? kRaggedPairs : kRaggedCtas;
+  P.r_max = (int)((long long)T * d.n_h / P.rows) + std::min(B, T);
+  size_t o = 256;
+  P.vs = o;         o = align_up(o + sizeof(int) * ((size_t)P.r_max + 1), 256);
+  P.pc = o;         o = align_up(o + sizeof(int) * ((size_t)P.r_max + 1), 256);
+  P.worker_seg = o; o = align_up(o + sizeof(int) * ((size_t)P.cap + 1), 256);
+  P.segs = o;       o = align_up(o + sizeof(RSeg) * ((size_t)P.cap + P.r_max), 256);
+  P.split = o;      o = align_up(o + sizeof(int) * ((size_t)P.cap + 1), 256);
+  P.part_o = o;     o = align_up(o + sizeof(float) * 2 * P.cap * P.rows * (size_t)d.d_c, 256);
+  P.part_ml = o;    o = align_up(o + sizeof(float2) * 2 * P.cap * P.rows, 256);
+  P.total = o;
+  return P;
+}
+
+mla_status check_ragged(const mla_dims* dims, int B, int T) {
+  mla_status s = check_dims(dims);
+  if (s != MLA_OK) return s;
+  if (B <= 0 || T < 0) return MLA_ERR_INVALID_ARG;
+  // One shared position key (a per-head one has no dense score product); row
+  // and row-block counts in 32 bits.
+  if (dims->rope_key_per_head || B > kRaggedMaxB || (long long)T * dims->n_h > INT_MAX - ragged_tc::ROWS)
+    return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+// RoPE frequencies as turns per position.
+step::Rope rope_table(const mla_dims& d) {
+  static thread_local step::Rope last;
+  static thread_local float last_base = 0.f;
+  if (last.half != d.d_r / 2 || last_base != d.rope_base) {
+    last.half = d.d_r / 2;
+    last_base = d.rope_base;
+    for (int i = 0; i < last.half; ++i)
+      last.turns[i] = pow((double)d.rope_base, -2.0 * i / d.d_r) / 6.283185307179586476925286766559;
+  }
+  return last;
+}
+
+template <int NPV>
+cudaError_t launch_ragged_tc(const CUtensorMap& mapS, const CUtensorMap& mapV, const ragged_tc::Args& a, int W,
+                             cudaStream_t st) {
+  auto kfn = ragged_tc::attn_ragged_kernel<NPV>;
+  cudaError_t e = set_smem_once(kfn, ragged_tc::SMEM_BYTES);
+  if (e) return e;
+  return launch_pdl(kfn, dim3(2 * W), dim3(ragged_tc::THREADS), ragged_tc::SMEM_BYTES, st, mapS, mapV, a);
+}
+
+template <int NG>
+cudaError_t launch_ragged_simt(const ragged_simt::Args& a, int W, cudaStream_t st) {
+  auto kfn = ragged_simt::attn_ragged_simt_kernel<NG>;
+  const size_t sm = ragged_simt::smem_bytes(a.d_c, a.d_r);
+  cudaError_t e = set_smem_once(kfn, ragged_simt::smem_bytes(512, 64));  // the largest of every width
+  if (e) return e;
+  return launch_pdl(kfn, dim3(W), dim3(ragged_simt::THREADS), sm, st, a);
+}
+
+// Schedule, attention, merge of the row blocks in pieces.
+mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, long long q_hs, const int32_t* q_start,
+                              const int32_t* kv_len, const int32_t* page_table, int B, int T, int max_pages,
+                              int num_pages, const void* cache, void* out, float* lse, void* ws, const RaggedPlan& P,
+                              cudaStream_t st) {
+  const bool tc = d.dtype == MLA_BF16;
+  const int W = std::max(1, std::min(P.cap, tc ? num_sms() / 2 : num_sms()));
+  const float scale =
+      (float)((d.softmax_scale > 0.f ? (double)d.softmax_scale : 1.0 / sqrt((double)(d.d_h + d.d_r))) * kLog2e);
+  const RaggedSched S{at<int>(ws, P.vs), at<int>(ws, P.pc), at<int>(ws, P.worker_seg), at<RSeg>(ws, P.segs),
+                      at<int>(ws, P.split)};
+  const RaggedOut o{out, lse, at<float>(ws, P.part_o), at<float2>(ws, P.part_ml), d.d_c};
+  int* err = at<int>(ws, P.hdr);
+  cudaError_t e;
+  {
+    const int ints = (int)std::min<long long>(B + 1 + 2LL * (P.r_max + 1), kRaggedSmemInts);
+    const RaggedSchedArgs a{q_start, kv_len, B, T, d.n_h, P.rows, W, max_pages, P.r_max,
+                            tc ? kBlockTilesTc : kBlockTilesSimt, S, err, ints};
+    if ((e = set_smem_once(ragged_sched_kernel, sizeof(int) * (size_t)kRaggedSmemInts))) return cuda_status(e);
+    ++g_launches;
+    ragged_sched_kernel<<<1, P.r_max > 1024 ? 1024 : 256, sizeof(int) * (size_t)ints, st>>>(a);
+    if ((e = cudaGetLastError())) return cuda_status(e);
+  }
+  ++g_launches;
+  prof_mark(st, true);
+  if (tc) {
+    ragged_tc::Args a{static_cast<const __nv_bfloat16*>(q), q_ts, q_hs, page_table, max_pages, num_pages, d.n_h, d.d_c,
+                      d.d_c + d.d_r, scale, q_hs == d.d_c + d.d_r && q_ts == d.n_h * q_hs, S, o, err};
+    // Score ring: 32-row boxes (one CTA's keys of a page); latent ring: 64-row boxes.
+    CUtensorMap mapS, mapV;
+    const long long rows = (long long)num_pages * d.page_size;
+    if (!encode_cache_map(&mapS, cache, a.q_row, rows, 32) || !encode_cache_map(&mapV, cache, a.q_row, rows, 64))
+      return MLA_ERR_CUDA;
+    switch (d.d_c / 128) {
+      case 1: e = launch_ragged_tc<1>(mapS, mapV, a, W, st); break;
+      case 2: e = launch_ragged_tc<2>(mapS, mapV, a, W, st); break;
+      case 3: e = launch_ragged_tc<3>(mapS, mapV, a, W, st); break;
+      default: e = launch_ragged_tc<4>(mapS, mapV, a, W, st); break;
+    }
+  } else {
+    ragged_simt::Args a{static_cast<const float*>(q), q_ts, q_hs, static_cast<const float*>(cache), page_table,
+                        max_pages, num_pages, d.n_h, d.d_c, d.d_r, scale, S, o, err};
+    if (d.d_c <= 64) e = launch_ragged_simt<1>(a, W, st);
+    else if (d.d_c <= 128) e = launch_ragged_simt<2>(a, W, st);
+    else if (d.d_c <= 256) e = launch_ragged_simt<4>(a, W, st);
+    else e = launch_ragged_simt<8>(a, W, st);
+  }
+  if (e) return cuda_status(e);
+  prof_mark(st, false);
+  ++g_launches;
+  const dim3 grid(W, ceil_div(d.d_c, kCombineCols));
+  if (tc) e = launch_pdl(ragged_combine_kernel<__nv_bfloat16, ragged_tc::ROWS>, grid, dim3(kCombineThreads), 0, st, S, o, W);
+  else e = launch_pdl(ragged_combine_kernel<float, ragged_simt::ROWS>, grid, dim3(kCombineThreads), 0, st, S, o, W);
+  return cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_plan_step(const int32_t* new_len, const int32_t* past_len, int B, const int32_t* free_pages, int n_free,
+                         int32_t* page_table, int max_pages, int num_pages, int32_t* q_start, int32_t* kv_len,
+                         int32_t* seq_idx, int32_t* pos, int64_t* slot, int rows, int32_t* counts,
+                         int32_t* device_error, cudaStream_t stream) {
+  if (B <= 0 || n_free < 0 || max_pages <= 0 || num_pages <= 0 || rows < 0) return MLA_ERR_INVALID_ARG;
+  if (!new_len || !past_len || !page_table || !q_start || !kv_len || !counts || (n_free > 0 && !free_pages) ||
+      (rows > 0 && (!seq_idx || !pos || !slot)))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(slot, 8) || !aligned(new_len, 4) || !aligned(past_len, 4) || !aligned(free_pages, 4) ||
+      !aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(seq_idx, 4) ||
+      !aligned(pos, 4) || !aligned(counts, 4) || !aligned(device_error, 4))
+    return MLA_ERR_INVALID_ARG;
+  // Sums and positions in 32 bits.
+  if (B > step::PLAN_MAX_B || rows == INT_MAX || n_free == INT_MAX || max_pages > INT_MAX / 64 - 1)
+    return MLA_ERR_UNSUPPORTED;
+  const step::PlanArgs a{new_len, past_len, free_pages, page_table, q_start, kv_len,    seq_idx, pos,
+                         slot,    counts,   device_error, B,        n_free,  max_pages, num_pages, rows};
+  const size_t sm = sizeof(uint32_t) * 2 * ((size_t)B + 1);
+  cudaError_t e = set_smem_once(step::plan_kernel, sizeof(uint32_t) * 2 * ((size_t)step::PLAN_MAX_B + 1));
+  if (e) return cuda_status(e);
+  g_launches = 1;
+  const int ctas = std::min(num_sms(), ceil_div(std::max(rows, B + 1), step::PLAN_THREADS));
+  step::plan_kernel<<<ctas, step::PLAN_THREADS, sm, stream>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+mla_status mla_append_normed(const mla_dims* dims, const void* kv, int64_t kv_stride, const void* kv_gamma,
+                             const void* cq, int64_t cq_stride, const void* cq_gamma, void* cq_out,
+                             int64_t cq_out_stride, float eps, const int32_t* pos, const int64_t* slot, void* cache,
+                             int num_pages, int T, int32_t* device_error, cudaStream_t stream) {
+  mla_status s = check_dims(dims);
+  if (s != MLA_OK) return s;
+  const mla_dims& d = *dims;
+  const int d_cr = cache_row(d);
+  if (T < 0 || num_pages <= 0 || !(eps >= 0.f) || kv_stride < d_cr) return MLA_ERR_INVALID_ARG;
+  if ((cq != nullptr) != (cq_out != nullptr) || (!cq && cq_gamma)) return MLA_ERR_INVALID_ARG;
+  if (cq && (d.d_cq <= 0 || cq_stride < d.d_cq || cq_out_stride < d.d_cq)) return MLA_ERR_INVALID_ARG;
+  if (T == 0) return MLA_OK;
+  if (!kv || !pos || !slot || !cache) return MLA_ERR_INVALID_ARG;
+  const size_t e = esize(d);
+  if (!aligned(kv, e) || !aligned(kv_gamma, e) || !aligned(cq, e) || !aligned(cq_gamma, e) || !aligned(cq_out, e) ||
+      !aligned(pos, 4) || !aligned(slot, 8) || !aligned(cache, 16) || !aligned(device_error, 4))
+    return MLA_ERR_INVALID_ARG;
+  step::NormAppendArgs a{};
+  a.kv = kv; a.kv_gamma = kv_gamma; a.kv_stride = kv_stride;
+  a.cq = cq; a.cq_gamma = cq_gamma; a.cq_stride = cq_stride;
+  a.cq_out = cq_out; a.cq_out_stride = cq_out_stride;
+  a.pos = pos; a.slot = slot; a.cache = cache; a.num_slots = (long long)num_pages * d.page_size;
+  a.err = device_error;
+  a.T = T; a.d_c = d.d_c; a.d_cr = d_cr; a.d_cq = cq ? d.d_cq : 0;
+  a.eps = eps;
+  a.rope = rope_table(d);
+  // 16-byte accesses where every row and width allows them.
+  const long long ve = 16 / (long long)e;
+  bool vec = aligned(kv, 16) && aligned(kv_gamma, 16) && kv_stride % ve == 0 && d.d_c % ve == 0 && d_cr % ve == 0;
+  if (cq)
+    vec = vec && aligned(cq, 16) && aligned(cq_gamma, 16) && aligned(cq_out, 16) && cq_stride % ve == 0 &&
+          cq_out_stride % ve == 0 && d.d_cq % ve == 0;
+  const long long warps = (long long)T * (cq ? 2 : 1);
+  const unsigned ctas = (unsigned)((warps + step::NORM_THREADS / 32 - 1) / (step::NORM_THREADS / 32));
+  g_launches = 1;
+  if (d.dtype == MLA_BF16) {
+    if (vec) step::norm_append_kernel<__nv_bfloat16, true><<<ctas, step::NORM_THREADS, 0, stream>>>(a);
+    else step::norm_append_kernel<__nv_bfloat16, false><<<ctas, step::NORM_THREADS, 0, stream>>>(a);
+  } else {
+    if (vec) step::norm_append_kernel<float, true><<<ctas, step::NORM_THREADS, 0, stream>>>(a);
+    else step::norm_append_kernel<float, false><<<ctas, step::NORM_THREADS, 0, stream>>>(a);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_stride, const void* gamma, float eps,
+                               const int32_t* pos, void* qc_out, int64_t qc_token_stride, int64_t qc_head_stride,
+                               void* qr_out, int64_t qr_token_stride, int64_t qr_head_stride, int T,
+                               cudaStream_t stream) {
+  mla_status s = check_dims(dims);
+  if (s != MLA_OK) return s;
+  const mla_dims& d = *dims;
+  if (T < 0 || !(eps >= 0.f) || q_stride < (long long)d.n_h * (d.d_h + d.d_r) || qc_head_stride < d.d_h ||
+      qr_head_stride < d.d_r || qc_token_stride < (d.n_h - 1) * qc_head_stride + d.d_h ||
+      qr_token_stride < (d.n_h - 1) * qr_head_stride + d.d_r)
+    return MLA_ERR_INVALID_ARG;
+  if (T == 0) return MLA_OK;
+  if (!q || !pos || !qc_out || !qr_out) return MLA_ERR_INVALID_ARG;
+  const size_t e = esize(d);
+  if (!aligned(q, e) || !aligned(gamma, e) || !aligned(pos, 4) || !aligned(qc_out, e) || !aligned(qr_out, e))
+    return MLA_ERR_INVALID_ARG;
+  const int ve = 16 / (int)e;
+  const bool vec = aligned(q, 16) && aligned(gamma, 16) && aligned(qc_out, 16) && aligned(qr_out, 16) &&
+                   d.d_h % ve == 0 && d.d_r % ve == 0 && q_stride % ve == 0 && qc_token_stride % ve == 0 &&
+                   qc_head_stride % ve == 0 && qr_token_stride % ve == 0 && qr_head_stride % ve == 0;
+  step::QueryArgs a{};
+  a.q = q; a.gamma = gamma; a.qc = qc_out; a.qr = qr_out; a.pos = pos;
+  a.q_stride = q_stride;
+  a.qc_ts = qc_token_stride; a.qc_hs = qc_head_stride;
+  a.qr_ts = qr_token_stride; a.qr_hs = qr_head_stride;
+  a.T = T; a.n_h = d.n_h; a.d_h = d.d_h; a.d_r = d.d_r;
+  a.eps = eps;
+  a.rope = rope_table(d);
+  const int nv = vec ? d.d_h / ve : d.d_h;
+  a.group = 4;
+  while (a.group < 32 && a.group < nv) a.group *= 2;
+  // Heads per block: two rounds of the block's lane groups, so that a few
+  // tokens' heads still spread over the GPU.
+  a.hpb = 2 * (step::QUERY_THREADS / a.group);
+  const dim3 grid((unsigned)T, (unsigned)ceil_div(d.n_h, a.hpb));
+  g_launches = 1;
+  if (d.dtype == MLA_BF16) {
+    if (vec) step::query_norm_rope_kernel<__nv_bfloat16, true><<<grid, step::QUERY_THREADS, 0, stream>>>(a);
+    else step::query_norm_rope_kernel<__nv_bfloat16, false><<<grid, step::QUERY_THREADS, 0, stream>>>(a);
+  } else {
+    if (vec) step::query_norm_rope_kernel<float, true><<<grid, step::QUERY_THREADS, 0, stream>>>(a);
+    else step::query_norm_rope_kernel<float, false><<<grid, step::QUERY_THREADS, 0, stream>>>(a);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+size_t mla_attend_ragged_workspace_bytes(const mla_dims* dims, int B, int T) {
+  if (check_ragged(dims, B, T) != MLA_OK) return 0;
+  return make_ragged_plan(*dims, B, T).total;
+}
+
+mla_status mla_attend_ragged(const mla_dims* dims, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                             const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int max_pages,
+                             int num_pages, const void* cache, void* out, float* lse, int B, int T, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream) {
+  mla_status s = check_ragged(dims, B, T);
+  if (s != MLA_OK) return s;
+  const mla_dims& d = *dims;
+  if (max_pages <= 0 || num_pages <= 0 || num_pages > INT_MAX / 64 || max_pages > INT_MAX / 64 ||
+      q_head_stride < d.d_c + d.d_r || q_token_stride < (d.n_h - 1) * q_head_stride + d.d_c + d.d_r)
+    return MLA_ERR_INVALID_ARG;
+  if (T == 0) return MLA_OK;
+  if (!q || !q_start || !kv_len || !page_table || !cache || !out || !workspace) return MLA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || !aligned(cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4))
+    return MLA_ERR_INVALID_ARG;
+  // The tensor-core path reads query rows in 16-byte pieces.
+  if (d.dtype == MLA_BF16 ? !aligned(q, 16) || q_token_stride % 8 || q_head_stride % 8 : !aligned(q, 4))
+    return MLA_ERR_INVALID_ARG;
+  const RaggedPlan P = make_ragged_plan(d, B, T);
+  if (workspace_bytes < P.total) return MLA_ERR_WORKSPACE;
+  g_launches = 0;
+  return attend_ragged_impl(d, q, q_token_stride, q_head_stride, q_start, kv_len, page_table, B, T, max_pages, num_pages,
+                            cache, out, lse, workspace, P, stream);
+}
+
+}  // extern "C"

@@ -27,14 +27,15 @@ EXPORTED = [
     "mla_last_launch_count", "mla_profile_begin", "mla_profile_end", "mla_append_latent_noalloc",
     "mla_decode_cp_workspace_bytes", "mla_decode_cp_partial", "mla_decode_cp_combine",
     "mla_selftest_wait_timeout", "mla_prefill_materialised_workspace_bytes", "mla_prefill_materialised",
-    "mla_decode_step_workspace_bytes", "mla_decode_step",
+    "mla_decode_step_workspace_bytes", "mla_decode_step", "mla_plan_step", "mla_append_normed",
+    "mla_query_norm_rope", "mla_attend_ragged_workspace_bytes", "mla_attend_ragged",
 ]
 APPEND_NOALLOC_MAX_T = 256
 
 
 class MlaError(RuntimeError):
-    def __init__(self, fn: str, code: int):
-        super().__init__(f"{fn} failed: {STATUS.get(code, code)}")
+    def __init__(self, fn: str, code: int, detail: str = ""):
+        super().__init__(f"{fn} failed: {STATUS.get(code, code)}" + (f" ({detail})" if detail else ""))
         self.code = code
 
 
@@ -56,6 +57,7 @@ def _load():
         raise ImportError(f"libmla.so not built ({LIB_PATH}); run head_latent_attention_append_b200/build.py")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, Z, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int
+    L, F = ctypes.c_int64, ctypes.c_float
     D = ctypes.POINTER(Dims)
     sig = {
         "mla_absorbed_weights_bytes": (Z, [D]),
@@ -82,6 +84,11 @@ def _load():
         "mla_selftest_wait_timeout": (S, [P, I, P]),
         "mla_prefill_materialised_workspace_bytes": (Z, [D, I, I]),
         "mla_prefill_materialised": (S, [P, P, P, I, I, P, P, I, I, P, Z, P]),
+        "mla_plan_step": (S, [P, P, I, P, I, P, I, I, P, P, P, P, P, I, P, P, P]),
+        "mla_append_normed": (S, [D, P, L, P, P, L, P, P, L, F, P, P, P, I, I, P, P]),
+        "mla_query_norm_rope": (S, [D, P, L, P, F, P, P, L, L, P, L, L, I, P]),
+        "mla_attend_ragged_workspace_bytes": (Z, [D, I, I]),
+        "mla_attend_ragged": (S, [D, P, L, L, P, P, P, I, I, P, P, P, I, I, P, Z, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -250,6 +257,134 @@ def decode_cp_combine(w: Weights, obar_parts, lse_parts, out, workspace, stream=
     _check("mla_decode_cp_combine", lib.mla_decode_cp_combine(
         w.handle, n_ranks, _ptr(obar_parts), _ptr(lse_parts), _ptr(out), B, n_q, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- ragged step
+# These calls check their tensors: sizes are taken from the shapes, so a wrong
+# shape, type or device would reach memory that is not the caller's.
+def _checked(fn: str, device, tensors):
+    """Each (name, tensor, dtype, shape, packed): on `device`, of that type and shape (None: any size); with
+    `packed` contiguous, else with a contiguous last axis."""
+    for name, t, dtype, shape, packed in tensors:
+        if t.dtype != dtype:
+            raise MlaError(fn, -1, f"{name}: {t.dtype}, expected {dtype}")
+        if t.device != device:
+            raise MlaError(fn, -1, f"{name} is on {t.device}, expected {device}")
+        got = t.shape
+        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+            raise MlaError(fn, -1, f"{name}: shape {tuple(got)}, expected {tuple('any' if w is None else w for w in shape)}")
+        if not (t.is_contiguous() if packed else (t.stride(-1) == 1 or got[-1] <= 1)):
+            raise MlaError(fn, -1, f"{name}: not contiguous" + ("" if packed else " along the last axis"))
+
+
+def _on(fn: str, device, stream):
+    """The raw stream for tensors of `device`, which has to be the current device."""
+    import torch
+    if device.type != "cuda":
+        raise MlaError(fn, -1, f"tensors are on {device}, expected a CUDA device")
+    if device.index != torch.cuda.current_device():
+        raise MlaError(fn, -1, f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def _step_of(t, axis: int, least: int) -> int:
+    """The stride of an axis; of one with a single entry, any will do."""
+    return t.stride(axis) if t.shape[axis] > 1 else least
+
+
+def _path_dtype(dims: Dims):
+    import torch
+    return torch.bfloat16 if dims.dtype == BF16 else torch.float32
+
+
+def plan_step(new_len, past_len, free_pages, page_table, num_pages: int, q_start, kv_len, seq_idx, pos, slot, counts,
+              device_error=None, stream=None):
+    """Page-table entries, slots and positions of a ragged step from the requests' lengths (include/mla.h)."""
+    import torch
+    fn, i32, dev = "mla_plan_step", torch.int32, new_len.device
+    B, rows = new_len.shape[0], seq_idx.shape[0]
+    _checked(fn, dev, (("new_len", new_len, i32, (B,), True), ("past_len", past_len, i32, (B,), True),
+                       ("free_pages", free_pages, i32, (None,), True), ("page_table", page_table, i32, (B, None), True),
+                       ("q_start", q_start, i32, (B + 1,), True), ("kv_len", kv_len, i32, (B,), True),
+                       ("seq_idx", seq_idx, i32, (rows,), True), ("pos", pos, i32, (rows,), True),
+                       ("slot", slot, torch.int64, (rows,), True), ("counts", counts, i32, (3,), True)))
+    if device_error is not None:
+        _checked(fn, dev, (("device_error", device_error, i32, (1,), True),))
+    st = _on(fn, dev, stream)
+    _check(fn, lib.mla_plan_step(
+        new_len.data_ptr(), past_len.data_ptr(), B, free_pages.data_ptr(), free_pages.shape[0], page_table.data_ptr(),
+        page_table.shape[1], num_pages, q_start.data_ptr(), kv_len.data_ptr(), seq_idx.data_ptr(), pos.data_ptr(),
+        slot.data_ptr(), rows, counts.data_ptr(), _ptr(device_error), st))
+
+
+def append_normed(dims: Dims, kv, kv_gamma, pos, slot, cache, eps: float = 1e-6, cq=None, cq_gamma=None, cq_out=None,
+                  device_error=None, stream=None):
+    """RMS norms of the latents, rotation of the position key and the write into the paged cache (include/mla.h)."""
+    import torch
+    fn, dt, dev = "mla_append_normed", _path_dtype(dims), kv.device
+    T, d_cr = kv.shape[0], dims.d_c + (dims.n_h if dims.rope_key_per_head else 1) * dims.d_r
+    _checked(fn, dev, (("kv", kv, dt, (T, d_cr), False), ("pos", pos, torch.int32, (T,), True),
+                       ("slot", slot, torch.int64, (T,), True),
+                       ("cache", cache, dt, (None, dims.page_size, d_cr), True)))
+    if kv_gamma is not None:
+        _checked(fn, dev, (("kv_gamma", kv_gamma, dt, (dims.d_c,), True),))
+    cs = os_ = 0
+    if cq is not None or cq_out is not None:
+        if cq is None or cq_out is None:
+            raise MlaError(fn, -1, "cq and cq_out go together")
+        _checked(fn, dev, (("cq", cq, dt, (T, dims.d_cq), False), ("cq_out", cq_out, dt, (T, dims.d_cq), False)))
+        cs, os_ = _step_of(cq, 0, dims.d_cq), _step_of(cq_out, 0, dims.d_cq)
+    if cq_gamma is not None:
+        _checked(fn, dev, (("cq_gamma", cq_gamma, dt, (dims.d_cq,), True),))
+    if device_error is not None:
+        _checked(fn, dev, (("device_error", device_error, torch.int32, (1,), True),))
+    st = _on(fn, dev, stream)
+    _check(fn, lib.mla_append_normed(
+        dims, kv.data_ptr(), _step_of(kv, 0, d_cr), _ptr(kv_gamma), _ptr(cq), cs, _ptr(cq_gamma), _ptr(cq_out), os_, eps,
+        pos.data_ptr(), slot.data_ptr(), cache.data_ptr(), cache.shape[0], T, _ptr(device_error), st))
+
+
+def query_norm_rope(dims: Dims, q, gamma, pos, qc_out, qr_out, eps: float = 1e-6, stream=None):
+    """RMS norm of every query head's content and rotation of its position part (include/mla.h)."""
+    import torch
+    fn, dt, dev = "mla_query_norm_rope", _path_dtype(dims), q.device
+    T, n_h, d_h, d_r = q.shape[0], dims.n_h, dims.d_h, dims.d_r
+    _checked(fn, dev, (("q", q, dt, (T, n_h, d_h + d_r), False), ("pos", pos, torch.int32, (T,), True),
+                       ("qc_out", qc_out, dt, (T, n_h, d_h), False), ("qr_out", qr_out, dt, (T, n_h, d_r), False)))
+    if n_h > 1 and q.stride(1) != d_h + d_r:
+        raise MlaError(fn, -1, "q: a token's heads have to be contiguous")
+    if gamma is not None:
+        _checked(fn, dev, (("gamma", gamma, dt, (d_h,), True),))
+    st = _on(fn, dev, stream)
+    ch, rh = _step_of(qc_out, 1, d_h), _step_of(qr_out, 1, d_r)
+    _check(fn, lib.mla_query_norm_rope(
+        dims, q.data_ptr(), _step_of(q, 0, n_h * (d_h + d_r)), _ptr(gamma), eps, pos.data_ptr(), qc_out.data_ptr(),
+        _step_of(qc_out, 0, n_h * ch), ch, qr_out.data_ptr(), _step_of(qr_out, 0, n_h * rh), rh, T, st))
+
+
+def attend_ragged_workspace_bytes(dims: Dims, B: int, T: int) -> int:
+    return lib.mla_attend_ragged_workspace_bytes(ctypes.byref(dims), B, T)
+
+
+def attend_ragged(dims: Dims, q, q_start, kv_len, page_table, cache, out, lse, workspace, stream=None):
+    """Absorbed attention of every request's new tokens over its paged cache (include/mla.h)."""
+    import torch
+    fn, dt, i32, dev = "mla_attend_ragged", _path_dtype(dims), torch.int32, q.device
+    T, B, n_h, d_cr = q.shape[0], kv_len.shape[0], dims.n_h, dims.d_c + dims.d_r
+    _checked(fn, dev, (("q", q, dt, (T, n_h, d_cr), False), ("q_start", q_start, i32, (B + 1,), True),
+                       ("kv_len", kv_len, i32, (B,), True), ("page_table", page_table, i32, (B, None), True),
+                       ("cache", cache, dt, (None, dims.page_size, d_cr), True),
+                       ("out", out, dt, (T, n_h, dims.d_c), True)))
+    if lse is not None:
+        _checked(fn, dev, (("lse", lse, torch.float32, (T, n_h), True),))
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise MlaError(fn, -1, f"workspace: contiguous memory on {dev} expected")
+    st = _on(fn, dev, stream)
+    hs = _step_of(q, 1, d_cr)
+    _check(fn, lib.mla_attend_ragged(
+        dims, q.data_ptr(), _step_of(q, 0, n_h * hs), hs, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
+        page_table.shape[1], cache.shape[0], cache.data_ptr(), out.data_ptr(), _ptr(lse), B, T, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), st))
 
 
 def selftest_wait_timeout(workspace, limit_us: int, stream=None):

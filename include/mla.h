@@ -303,6 +303,106 @@ mla_status mla_prefill_materialised(const mla_weights* w, const void* h, const i
                                     cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * A ragged serving step: every request brings its own number of new tokens (a
+ * decoding request one or a few, another a chunk of its prompt), all of them
+ * rows of one packed batch.  The pages describe single sequences and leave
+ * this to the caller; these calls are what a serving loop runs around the
+ * projections, on the cache layout above (64-token pages):
+ *
+ *   mla_plan_step        lengths -> page-table entries, slots, positions
+ *   mla_append_normed    RMS norms of the latents, rotation of the position
+ *                        key, write into the paged cache
+ *   mla_query_norm_rope  RMS norm of every query head, rotation of its
+ *                        position part
+ *   mla_attend_ragged    absorbed attention of all new tokens
+ *
+ * They take mla_dims instead of a weights handle.  Tensors that are read and
+ * tensors that are written must not overlap unless said otherwise.
+ *
+ * Row convention: the new tokens of request b are rows q_start[b] ..
+ * q_start[b+1] - 1 of every packed tensor, and sit at positions
+ * kv_len[b] - (q_start[b+1] - q_start[b]) .. kv_len[b] - 1.
+ * ------------------------------------------------------------------------- */
+
+/* Plan.  new_len[B] and past_len[B] count each request's new and cached
+ * tokens; page_table [B, max_pages] holds the pages of the cached ones, and
+ * free_pages [n_free] are pages no request uses.  Requests are admitted in
+ * order as long as their new tokens fit into `rows` rows and their new pages
+ * into the free list; the first that does not fit, and every one behind it, is
+ * refused (as if it had no new token).  Writes
+ *   page_table: the admitted requests' new pages, taken from free_pages in
+ *     order (entries ceil(past/64) .. ceil((past+new)/64)-1; no other entry);
+ *   q_start [B+1], kv_len [B] (cached tokens plus admitted new ones);
+ *   seq_idx, pos, slot [rows]: request, position and cache row
+ *     (page*64 + pos%64, int64) of every admitted token; rows behind the last
+ *     one get seq_idx -1, pos 0, slot -1;
+ *   counts [3]: requests admitted, their tokens, pages taken.
+ * A request with a negative length, or one longer than max_pages*64, counts as
+ * empty with kv_len 0; a page id outside [0, num_pages) gives slot -1; both OR
+ * 1 into *device_error (device int32, NULL to ignore, zeroed by the caller).
+ * B <= 16384, else MLA_ERR_UNSUPPORTED.  Needs no workspace. */
+mla_status mla_plan_step(const int32_t* new_len, const int32_t* past_len, int B,
+                         const int32_t* free_pages, int n_free, int32_t* page_table, int max_pages,
+                         int num_pages, int32_t* q_start, int32_t* kv_len, int32_t* seq_idx,
+                         int32_t* pos, int64_t* slot, int rows, int32_t* counts,
+                         int32_t* device_error, cudaStream_t stream);
+
+/* Normalised append.  Row t of kv (kv_stride elements apart, at least
+ * d_c + d_r; with per-head keys d_c + n_h*d_r) is an unnormalised latent and
+ * an unrotated position key, [c | k_R]; writes
+ *   cache row slot[t] = [c / sqrt(mean(c^2) + eps) * kv_gamma | RoPE_pos[t](k_R)]
+ * and, when cq is given, cq_out[t] = cq[t] / sqrt(mean(cq[t]^2) + eps) *
+ * cq_gamma (d_cq elements; strides in elements; cq_out may be cq).  A NULL
+ * gamma leaves that latent unnormalised.  Statistics, rotation and products are
+ * taken in 32 bits (angles in 64) and rounded once.  slot -1 leaves the cache
+ * alone; any other slot outside [0, num_pages*64) does too and ORs 1 into
+ * *device_error (may be NULL).  Slots other than -1 must differ.  Rows that
+ * start on 16-byte boundaries are moved fastest; any element alignment works. */
+mla_status mla_append_normed(const mla_dims* dims, const void* kv, int64_t kv_stride,
+                             const void* kv_gamma, const void* cq, int64_t cq_stride,
+                             const void* cq_gamma, void* cq_out, int64_t cq_out_stride, float eps,
+                             const int32_t* pos, const int64_t* slot, void* cache, int num_pages,
+                             int T, int32_t* device_error, cudaStream_t stream);
+
+/* Query norm and rotation.  Row (t, h) of q (q_stride elements per token,
+ * heads d_h + d_r apart) is [q_C (d_h) | q_R (d_r)]; writes
+ *   qc_out[t, h] = q_C / sqrt(mean(q_C^2) + eps) * gamma     (gamma [d_h], shared
+ *     by the heads; NULL: q_C as it is),
+ *   qr_out[t, h] = RoPE_pos[t](q_R),
+ * each with its own token and head strides (elements), so q_R can go straight
+ * into the [q~ | q_R] rows that the attention reads.  Outputs may be the same
+ * parts of q itself (same addresses and strides).  Rounded once, as above. */
+mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_stride,
+                               const void* gamma, float eps, const int32_t* pos, void* qc_out,
+                               int64_t qc_token_stride, int64_t qc_head_stride, void* qr_out,
+                               int64_t qr_token_stride, int64_t qr_head_stride, int T,
+                               cudaStream_t stream);
+
+/* Ragged attention.  q rows (t, h) are absorbed queries [q~ | q_R] (d_c + d_r
+ * values, unscaled; strides in elements, for bf16 multiples of 8 from a
+ * 16-byte aligned address).  Token i of request b sees the keys at positions
+ * 0 .. kv_len[b] - (q_start[b+1] - q_start[b]) + i (its own, already in the
+ * cache, included):
+ *   out[t, h] = sum_k alpha_k c_k,  alpha = softmax(s (q~ . c_k + q_R . k_R,k)),
+ * [T, n_h, d_c] in the cache's type, s as mla_dims.softmax_scale says, and,
+ * unless lse is NULL, lse[t, h] = log2 sum_k exp(...) (fp32), as
+ * mla_decode_cp_combine takes them.  A token whose position is negative sees
+ * nothing: zeros and -inf.  Rows outside [q_start[0], q_start[B]) are left as
+ * they are.  Cache rows that no query sees may hold anything.  q_start that
+ * decreases or leaves [0, T] computes nothing; a length outside
+ * [0, max_pages*64] is clamped; a page id outside [0, num_pages) is read as
+ * page 0; each sets MLA_ERR_DEVICE_BOUNDS in the workspace error word.
+ * Deterministic.  One shared RoPE key and B <= 16384 (else
+ * MLA_ERR_UNSUPPORTED).  Workspace: mla_attend_ragged_workspace_bytes, for at
+ * least this B and T. */
+size_t mla_attend_ragged_workspace_bytes(const mla_dims* dims, int B, int T);
+mla_status mla_attend_ragged(const mla_dims* dims, const void* q, int64_t q_token_stride,
+                             int64_t q_head_stride, const int32_t* q_start, const int32_t* kv_len,
+                             const int32_t* page_table, int max_pages, int num_pages,
+                             const void* cache, void* out, float* lse, int B, int T,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Status.
  * ------------------------------------------------------------------------- */
 /* Waits for `stream`, then returns the error recorded on the device by the
