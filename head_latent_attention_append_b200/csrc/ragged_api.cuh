@@ -7,7 +7,6 @@ namespace {
 // Workers of the ragged attention: CTA pairs on the tensor cores, CTAs on the
 // CUDA cores.  The caps size the partial slots.
 constexpr int kRaggedPairs = 80, kRaggedCtas = 160;
-static_assert(kRaggedPairs <= 160 && kRaggedCtas <= 160, "ragged_combine_kernel lists a piece per worker");
 // What changing query rows costs a worker, in tiles of 64 keys: the next rows'
 // load and this block's output (about 6 us against 0.9 us a tile on the tensor
 // cores; small against a tile on the CUDA cores).
@@ -28,7 +27,7 @@ RaggedPlan make_ragged_plan(const mla_dims& d, int B, int T) {
   P.pc = o;         o = align_up(o + sizeof(int) * ((size_t)P.r_max + 1), 256);
   P.worker_seg = o; o = align_up(o + sizeof(int) * ((size_t)P.cap + 1), 256);
   P.segs = o;       o = align_up(o + sizeof(RSeg) * ((size_t)P.cap + P.r_max), 256);
-  P.split = o;      o = align_up(o + sizeof(int) * ((size_t)P.cap + 1), 256);
+  P.split = o;      o = align_up(o + sizeof(int4) * (size_t)P.cap, 256);
   P.part_o = o;     o = align_up(o + sizeof(float) * 2 * P.cap * P.rows * (size_t)d.d_c, 256);
   P.part_ml = o;    o = align_up(o + sizeof(float2) * 2 * P.cap * P.rows, 256);
   P.total = o;
@@ -77,6 +76,41 @@ cudaError_t launch_ragged_simt(const ragged_simt::Args& a, int W, cudaStream_t s
   return launch_pdl(kfn, dim3(W), dim3(ragged_simt::THREADS), sm, st, a);
 }
 
+// Rows per block of the normalised append: one, until the blocks fill the GPU
+// eight times over; then each walks several.
+template <typename T>
+void launch_norm_append(const step::NormAppendArgs& a, bool vec, cudaStream_t st) {
+  const int ve = vec ? 16 / (int)sizeof(T) : 1, per = a.cq ? 1 : step::NORM_THREADS / 32;
+  const int grid = std::min(ceil_div(a.T, per), 8 * num_sms());
+  const bool small = a.d_c <= 2 * 32 * ve && a.d_cq <= 2 * 96 * ve;  // two vectors a thread
+  if (!vec) step::norm_append_kernel<T, false, 4><<<grid, step::NORM_THREADS, 0, st>>>(a);
+  else if (small) step::norm_append_kernel<T, true, 2><<<grid, step::NORM_THREADS, 0, st>>>(a);
+  else step::norm_append_kernel<T, true, 4><<<grid, step::NORM_THREADS, 0, st>>>(a);
+}
+
+template <typename T, bool kVec, int G, int VPL>
+void launch_query(step::QueryArgs& a, cudaStream_t st) {
+  // Heads per block: all of a token's, unless that leaves the GPU with fewer
+  // than sixteen blocks an SM; then fewer, in whole steps.
+  const int step_heads = 2 * (step::QUERY_THREADS / G), steps = ceil_div(a.n_h, step_heads);
+  const int want = ceil_div(16 * num_sms(), a.T), parts = std::max(1, std::min(steps, want));
+  a.hpb = step_heads * ceil_div(steps, parts);
+  step::query_norm_rope_kernel<T, kVec, G, VPL>
+      <<<dim3((unsigned)a.T, (unsigned)ceil_div(a.n_h, a.hpb)), step::QUERY_THREADS, 0, st>>>(a);
+}
+template <typename T>
+void launch_query(step::QueryArgs& a, bool vec, cudaStream_t st) {
+  const int ve = 16 / (int)sizeof(T), parts = vec ? a.d_r / ve : a.d_r / 2;  // vectors or pairs of a position part
+  for (a.rope_shift = 0; (1 << a.rope_shift) < parts;) ++a.rope_shift;
+  if (!vec) return launch_query<T, false, 32, 4>(a, st);
+  const int nv = a.d_h / ve;
+  if (nv <= 4) launch_query<T, true, 4, 1>(a, st);
+  else if (nv <= 8) launch_query<T, true, 8, 1>(a, st);
+  else if (nv <= 16) launch_query<T, true, 16, 1>(a, st);
+  else if (nv <= 32) launch_query<T, true, 32, 1>(a, st);
+  else launch_query<T, true, 32, 4>(a, st);
+}
+
 // Schedule, attention, merge of the row blocks in pieces.
 mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, long long q_hs, const int32_t* q_start,
                               const int32_t* kv_len, const int32_t* page_table, int B, int T, int max_pages,
@@ -87,7 +121,7 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
   const float scale =
       (float)((d.softmax_scale > 0.f ? (double)d.softmax_scale : 1.0 / sqrt((double)(d.d_h + d.d_r))) * kLog2e);
   const RaggedSched S{at<int>(ws, P.vs), at<int>(ws, P.pc), at<int>(ws, P.worker_seg), at<RSeg>(ws, P.segs),
-                      at<int>(ws, P.split)};
+                      at<int>(ws, P.hdr) + 1, at<int4>(ws, P.split)};
   const RaggedOut o{out, lse, at<float>(ws, P.part_o), at<float2>(ws, P.part_ml), d.d_c};
   int* err = at<int>(ws, P.hdr);
   cudaError_t e;
@@ -128,8 +162,8 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
   prof_mark(st, false);
   ++g_launches;
   const dim3 grid(W, ceil_div(d.d_c, kCombineCols));
-  if (tc) e = launch_pdl(ragged_combine_kernel<__nv_bfloat16, ragged_tc::ROWS>, grid, dim3(kCombineThreads), 0, st, S, o, W);
-  else e = launch_pdl(ragged_combine_kernel<float, ragged_simt::ROWS>, grid, dim3(kCombineThreads), 0, st, S, o, W);
+  if (tc) e = launch_pdl(ragged_combine_kernel<__nv_bfloat16, ragged_tc::ROWS>, grid, dim3(kCombineThreads), 0, st, S, o);
+  else e = launch_pdl(ragged_combine_kernel<float, ragged_simt::ROWS>, grid, dim3(kCombineThreads), 0, st, S, o);
   return cuda_status(e);
 }
 
@@ -195,16 +229,9 @@ mla_status mla_append_normed(const mla_dims* dims, const void* kv, int64_t kv_st
   if (cq)
     vec = vec && aligned(cq, 16) && aligned(cq_gamma, 16) && aligned(cq_out, 16) && cq_stride % ve == 0 &&
           cq_out_stride % ve == 0 && d.d_cq % ve == 0;
-  const long long warps = (long long)T * (cq ? 2 : 1);
-  const unsigned ctas = (unsigned)((warps + step::NORM_THREADS / 32 - 1) / (step::NORM_THREADS / 32));
   g_launches = 1;
-  if (d.dtype == MLA_BF16) {
-    if (vec) step::norm_append_kernel<__nv_bfloat16, true><<<ctas, step::NORM_THREADS, 0, stream>>>(a);
-    else step::norm_append_kernel<__nv_bfloat16, false><<<ctas, step::NORM_THREADS, 0, stream>>>(a);
-  } else {
-    if (vec) step::norm_append_kernel<float, true><<<ctas, step::NORM_THREADS, 0, stream>>>(a);
-    else step::norm_append_kernel<float, false><<<ctas, step::NORM_THREADS, 0, stream>>>(a);
-  }
+  if (d.dtype == MLA_BF16) launch_norm_append<__nv_bfloat16>(a, vec, stream);
+  else launch_norm_append<float>(a, vec, stream);
   return cuda_status(cudaGetLastError());
 }
 
@@ -236,21 +263,9 @@ mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_st
   a.T = T; a.n_h = d.n_h; a.d_h = d.d_h; a.d_r = d.d_r;
   a.eps = eps;
   a.rope = rope_table(d);
-  const int nv = vec ? d.d_h / ve : d.d_h;
-  a.group = 4;
-  while (a.group < 32 && a.group < nv) a.group *= 2;
-  // Heads per block: two rounds of the block's lane groups, so that a few
-  // tokens' heads still spread over the GPU.
-  a.hpb = 2 * (step::QUERY_THREADS / a.group);
-  const dim3 grid((unsigned)T, (unsigned)ceil_div(d.n_h, a.hpb));
   g_launches = 1;
-  if (d.dtype == MLA_BF16) {
-    if (vec) step::query_norm_rope_kernel<__nv_bfloat16, true><<<grid, step::QUERY_THREADS, 0, stream>>>(a);
-    else step::query_norm_rope_kernel<__nv_bfloat16, false><<<grid, step::QUERY_THREADS, 0, stream>>>(a);
-  } else {
-    if (vec) step::query_norm_rope_kernel<float, true><<<grid, step::QUERY_THREADS, 0, stream>>>(a);
-    else step::query_norm_rope_kernel<float, false><<<grid, step::QUERY_THREADS, 0, stream>>>(a);
-  }
+  if (d.dtype == MLA_BF16) launch_query<__nv_bfloat16>(a, vec, stream);
+  else launch_query<float>(a, vec, stream);
   return cuda_status(cudaGetLastError());
 }
 

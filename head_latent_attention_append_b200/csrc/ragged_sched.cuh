@@ -37,8 +37,13 @@ struct RaggedSched {
   int* pc;          // [R+1] first segment of each row block
   int* worker_seg;  // [W+1] first segment of each worker
   RSeg* segs;       // [W+R]
-  int* split;       // [1+W] count, then the first segment of each row block in pieces
+  int* split_n;     // row blocks in pieces, and
+  int4* split;      // [W] for each: first row, rows, worker of the first piece, pieces (one per worker from there on)
 };
+
+// The partial slot of piece k of a row block whose first piece is worker w0's:
+// that one is its worker's last segment, the others are their workers' first.
+__host__ __device__ __forceinline__ int ragged_slot(int w0, int k) { return k > 0 ? 2 * (w0 + k) : 2 * w0 + 1; }
 
 struct RaggedSchedArgs {
   const int32_t* q_start;  // [B+1]
@@ -86,7 +91,7 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   const int tid = threadIdx.x, nt = blockDim.x;
   if (tid == 0) {
     *a.err = 0;
-    a.s.split[0] = 0;
+    *a.s.split_n = 0;
   }
   __syncthreads();
   // Starts that leave [0, T] or decrease leave nothing to compute; a length
@@ -136,7 +141,14 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   if (tid == 0) vs[R] = total;
   const int W = min(a.W, total);  // every worker's share has at least one tile
   // The worker whose share [w total / W, (w + 1) total / W) holds tile x.
-  auto owner = [&](int x) { return (int)((((long long)x + 1) * W - 1) / total); };
+  const bool narrow = (long long)total * W < 0x7fffffffLL;  // 64-bit divisions cost a microsecond here
+  auto owner = [&](int x) {
+    return narrow ? (int)(((unsigned)(x + 1) * (unsigned)W - 1u) / (unsigned)total)
+                  : (int)((((long long)x + 1) * W - 1) / total);
+  };
+  auto share = [&](int w) {  // first tile of worker w's share
+    return narrow ? (int)((unsigned)w * (unsigned)total / (unsigned)W) : (int)((long long)w * total / W);
+  };
   __syncthreads();
   for (int rb = tid; rb < R; rb += nt) pc[rb] = owner(vs[rb + 1] - 1) - owner(vs[rb] + a.block_tiles) + 1;
   __syncthreads();
@@ -147,18 +159,17 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
     const int rb = find_le(pc, R, s), k = s - pc[rb], pieces = pc[rb + 1] - pc[rb];
     const int first = vs[rb] + a.block_tiles, w = owner(first) + k;
     RSeg g = block(rb);
-    const long long lo = (long long)w * total / W, hi = (long long)(w + 1) * total / W;
-    g.t_lo = (int)max(lo - first, 0LL);
-    g.t_hi = (int)min(hi, (long long)vs[rb + 1]) - first;
+    g.t_lo = max(share(w) - first, 0);
+    g.t_hi = min(share(w + 1), vs[rb + 1]) - first;
     // Only the first and the last segment of a worker can be pieces.
-    g.slot = pieces == 1 ? -1 : (k > 0 ? 2 * w : 2 * w + 1);
+    g.slot = pieces == 1 ? -1 : ragged_slot(w - k, k);
     g.pad[0] = g.pad[1] = g.pad[2] = 0;
     a.s.segs[s] = g;
     const int before = k > 0 ? w - 1 : (rb > 0 ? owner(vs[rb] - 1) : -1);  // the previous segment's worker
     for (int v = before + 1; v <= w; ++v) a.s.worker_seg[v] = s;
     if (s == nseg - 1)
       for (int v = w + 1; v <= a.W; ++v) a.s.worker_seg[v] = nseg;
-    if (k == 0 && pieces > 1) a.s.split[1 + atomicAdd(&a.s.split[0], 1)] = s;
+    if (k == 0 && pieces > 1) a.s.split[atomicAdd(a.s.split_n, 1)] = make_int4(g.row0, g.nrows, w, pieces);
   }
 }
 
@@ -167,14 +178,6 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
 // by column, the piece's O / l (32 bits, rows contiguous, so that both sides
 // move whole lines), and its (m, l) per row, in base 2:
 //   m = max m_s,  l = sum 2^(m_s - m) l_s,  o = sum 2^(m_s - m) l_s N_s / l.
-// One CTA merges 32 columns of a row block, its pieces in order.
-// A row that sees no key of a piece (or none at all) has m = -inf and l = 0:
-// its weights are taken relative to 0, its output is 0 and its lse -inf.  A
-// NaN among its scores makes l, and with it the row, NaN.
-__device__ __forceinline__ float ref_max(float m) { return m == -INFINITY ? 0.f : m; }
-__device__ __forceinline__ float row_inv(float l) { return l == 0.f ? 0.f : 1.f / l; }
-__device__ __forceinline__ float row_lse(float ref, float l) { return l == 0.f ? -INFINITY : ref + log2f(l); }
-
 struct RaggedOut {
   void* out;       // [T * n_h][d_c]
   float* lse;      // [T * n_h] or null
@@ -183,58 +186,100 @@ struct RaggedOut {
   int d_c;
 };
 
-constexpr int kCombineCols = 32, kCombineThreads = 256;
+// A row that sees no key of a piece (or none at all) has m = -inf and l = 0:
+// its weights are taken relative to 0, its output is 0 and its lse -inf.  A
+// NaN among its scores makes l, and with it the row, NaN.
+__device__ __forceinline__ float ref_max(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ float row_inv(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float row_lse(float ref, float l) { return l == 0.f ? -INFINITY : ref + log2f(l); }
+
+// One CTA merges kCombineCols columns of a row block, its pieces in order.
+// Bound by latency (a few pieces of a few hundred KB in all, from L2), so a
+// thread asks for kBatch pieces at once (four rows, 16 bytes, of each).  The
+// rows' weights of a batch are made once per CTA, in shared memory.
+constexpr int kCombineCols = 32, kCombineThreads = 256, kBatch = 8;
 
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(kCombineThreads) ragged_combine_kernel(RaggedSched S, RaggedOut o, int W) {
+__global__ void __launch_bounds__(kCombineThreads) ragged_combine_kernel(RaggedSched S, RaggedOut o) {
   sm100::pdl_wait();
   sm100::pdl_trigger();
-  constexpr int SUB = kCombineThreads / ROWS;   // threads per row
-  constexpr int CPT = kCombineCols / SUB;       // columns per thread
-  __shared__ int slots[2 * 160];
+  constexpr int QUADS = ROWS / 4 * kCombineCols / kCombineThreads;  // (four rows, column) items per thread
+  __shared__ __align__(16) float coef[kBatch][ROWS];
+  __shared__ float top[ROWS], sum[ROWS];
   __shared__ float tile[ROWS][kCombineCols + 1];
-  if ((int)blockIdx.x >= S.split[0]) return;
-  const int s0 = S.split[1 + blockIdx.x], nall = S.worker_seg[W];
-  const RSeg g = S.segs[s0];
-  const int tid = threadIdx.x;
-  // The pieces of a row block follow one another, at most one per worker.
-  int np = 0;
-  for (int k0 = 0; k0 < W; k0 += kCombineThreads) {
-    const int s = s0 + k0 + tid;
-    const bool mine = s < nall && k0 + tid < W && S.segs[s].row0 == g.row0;
-    if (mine) slots[k0 + tid] = S.segs[s].slot;
-    np += __syncthreads_count(mine);
+  const int4 e = S.split[blockIdx.x];  // before the count is known: the entry exists
+  if ((int)blockIdx.x >= *S.split_n) return;
+  const int row0 = e.x, nrows = e.y, w0 = e.z, np = e.w, tid = threadIdx.x;
+  const int col0 = blockIdx.y * kCombineCols, cols = min(kCombineCols, o.d_c - col0);
+  for (int r = tid; r < nrows; r += kCombineThreads) {
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < np; ++k) m = fmaxf(m, __ldcg(&o.part_ml[(long long)ragged_slot(w0, k) * ROWS + r]).x);
+    top[r] = ref_max(m);
+    sum[r] = 0.f;
   }
-  const int row = tid % ROWS, sub = tid / ROWS, c0 = blockIdx.y * kCombineCols + sub * CPT;
-  float acc[CPT];
+  const int nq = (nrows + 3) / 4, items = nq * cols;  // consecutive items are consecutive in a slot's column
+  int off[QUADS], rq[QUADS];
+  float4 acc[QUADS];
 #pragma unroll
-  for (int c = 0; c < CPT; ++c) acc[c] = 0.f;
-  if (row < g.nrows) {
-    float m = -INFINITY, l = 0.f;
-    for (int k = 0; k < np; ++k) m = fmaxf(m, __ldcg(&o.part_ml[(long long)slots[k] * ROWS + row]).x);
-    m = ref_max(m);
-    for (int k = 0; k < np; ++k) {
-      const float2 ml = __ldcg(&o.part_ml[(long long)slots[k] * ROWS + row]);
-      const float w = exp2f(ml.x - m) * ml.y;
-      const float* src = o.part_o + ((long long)slots[k] * o.d_c + c0) * ROWS + row;
-#pragma unroll
-      for (int c = 0; c < CPT; ++c)
-        if (c0 + c < o.d_c) acc[c] = fmaf(w, __ldcg(src + c * ROWS), acc[c]);
-      l += w;
-    }
-    const float inv = row_inv(l);
-#pragma unroll
-    for (int c = 0; c < CPT; ++c) acc[c] *= inv;
-    if (o.lse && blockIdx.y == 0 && sub == 0) o.lse[(long long)g.row0 + row] = row_lse(m, l);
+  for (int i = 0; i < QUADS; ++i) {
+    const int x = tid + i * kCombineThreads, c = x / nq;
+    rq[i] = 4 * (x - c * nq);
+    off[i] = x < items ? (col0 + c) * ROWS + rq[i] : -1;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-#pragma unroll
-  for (int c = 0; c < CPT; ++c) tile[row][sub * CPT + c] = acc[c];
   __syncthreads();
-  const int cols = min(kCombineCols, o.d_c - (int)blockIdx.y * kCombineCols);
-  T* const dst = static_cast<T*>(o.out) + (long long)g.row0 * o.d_c + blockIdx.y * kCombineCols;
-  for (int i = tid; i < g.nrows * kCombineCols; i += kCombineThreads) {
-    const int r = i / kCombineCols, c = i % kCombineCols;
-    if (c < cols) dst[(long long)r * o.d_c + c] = from_f32<T>(tile[r][c]);
+  for (int k0 = 0; k0 < np; k0 += kBatch) {
+    const int kn = min(kBatch, np - k0);
+    for (int x = tid; x < kn * nrows; x += kCombineThreads) {
+      const int k = x / nrows, r = x - k * nrows;
+      const float2 ml = __ldcg(&o.part_ml[(long long)ragged_slot(w0, k0 + k) * ROWS + r]);
+      coef[k][r] = exp2f(ml.x - top[r]) * ml.y;
+    }
+    __syncthreads();
+    for (int r = tid; r < nrows; r += kCombineThreads) {
+      float l = sum[r];
+      for (int k = 0; k < kn; ++k) l += coef[k][r];
+      sum[r] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i) {
+      if (off[i] < 0) continue;
+      float4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k < kn)
+          v[k] = __ldcg(reinterpret_cast<const float4*>(o.part_o + (long long)ragged_slot(w0, k0 + k) * o.d_c * ROWS + off[i]));
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k < kn) {
+          const float4 c = *reinterpret_cast<const float4*>(&coef[k][rq[i]]);
+          acc[i].x = fmaf(c.x, v[k].x, acc[i].x);
+          acc[i].y = fmaf(c.y, v[k].y, acc[i].y);
+          acc[i].z = fmaf(c.z, v[k].z, acc[i].z);
+          acc[i].w = fmaf(c.w, v[k].w, acc[i].w);
+        }
+    }
+    __syncthreads();
+  }
+  // The rows behind nrows of a last group of four are never written to a slot;
+  // what they leave in the tile is not stored.
+#pragma unroll
+  for (int i = 0; i < QUADS; ++i)
+    if (off[i] >= 0) {
+      const int c = off[i] / ROWS - col0;
+      tile[rq[i]][c] = acc[i].x;
+      tile[rq[i] + 1][c] = acc[i].y;
+      tile[rq[i] + 2][c] = acc[i].z;
+      tile[rq[i] + 3][c] = acc[i].w;
+    }
+  __syncthreads();
+  if (o.lse && blockIdx.y == 0)
+    for (int r = tid; r < nrows; r += kCombineThreads) o.lse[(long long)row0 + r] = row_lse(top[r], sum[r]);
+  T* const dst = static_cast<T*>(o.out) + (long long)row0 * o.d_c + col0;
+  for (int x = tid; x < nrows * kCombineCols; x += kCombineThreads) {
+    const int r = x / kCombineCols, c = x % kCombineCols;
+    if (c < cols) dst[(long long)r * o.d_c + c] = from_f32<T>(tile[r][c] * row_inv(sum[r]));
   }
 }
 

@@ -187,10 +187,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
 
 // ---------------------------------------------------------- norms, rotation
 // 16-byte vectors where every row starts on a 16-byte boundary and every
-// width is whole vectors (VE elements each), else single elements.
+// width is whole vectors (VE elements each), else single elements.  The values
+// are worked on two at a time (packed 32-bit multiplies and FMAs): these calls
+// move every byte once and would be bound by issued instructions otherwise.
 template <typename T, bool kVec>
 struct Vec {
   static constexpr int VE = kVec ? 16 / (int)sizeof(T) : 1;
+  static constexpr int NP = kVec ? VE / 2 : 1;  // pairs (a single element is one with 0)
   uint4 u;  // as it is stored: half the registers of its values in 32 bits
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (kVec) u = *reinterpret_cast<const uint4*>(p);
@@ -200,49 +203,51 @@ struct Vec {
     if constexpr (kVec) *reinterpret_cast<uint4*>(p) = u;
     else *p = from_f32<T>(__uint_as_float(u.x));
   }
-  __device__ __forceinline__ void get(float (&f)[VE]) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    if constexpr (kVec && sizeof(T) == 2) {
+  __device__ __forceinline__ void get(float2 (&f)[NP]) const {
+    if constexpr (!kVec) {
+      f[0] = make_float2(__uint_as_float(u.x), 0.f);
+    } else if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[q]));
-        f[2 * q] = v.x;
-        f[2 * q + 1] = v.y;
-      }
+      for (int q = 0; q < 4; ++q) f[q] = make_float2(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xffff0000u));
     } else {
-#pragma unroll
-      for (int q = 0; q < VE; ++q) f[q] = __uint_as_float(w[q]);
+      f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+      f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
     }
   }
-  __device__ __forceinline__ void set(const float (&f)[VE]) {
-    if constexpr (kVec && sizeof(T) == 2) {
+  __device__ __forceinline__ void set(const float2 (&f)[NP]) {
+    if constexpr (!kVec) {
+      u.x = __float_as_uint(f[0].x);
+    } else if constexpr (sizeof(T) == 2) {
       uint32_t w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
+        const __nv_bfloat162 h = __float22bfloat162_rn(f[q]);
         w[q] = *reinterpret_cast<const uint32_t*>(&h);
       }
       u = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if constexpr (kVec) {
-      u = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     } else {
-      u.x = __float_as_uint(f[0]);
+      u = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
     }
   }
-  // Adds the squares of the values times `by` to `ss`.
-  __device__ __forceinline__ void squares(float& ss, float by = 1.f) const {
-    float f[VE];
+  // Adds the squares of the values (times `by`, where it is not 1) to `ss`.
+  template <bool kScaled>
+  __device__ __forceinline__ void squares(float2& ss, float by) const {
+    float2 f[NP];
     get(f);
 #pragma unroll
-    for (int e = 0; e < VE; ++e) ss = fmaf(f[e] * by, f[e] * by, ss);
+    for (int e = 0; e < NP; ++e) {
+      if constexpr (kScaled) f[e] = __fmul2_rn(f[e], make_float2(by, by));
+      ss = __ffma2_rn(f[e], f[e], ss);
+    }
   }
   // The normalised values: x * inv * gamma, rounded once.
   __device__ __forceinline__ void norm(float inv, const Vec& g) {
-    float f[VE], h[VE];
+    float2 f[NP], h[NP];
     get(f);
     g.get(h);
 #pragma unroll
-    for (int e = 0; e < VE; ++e) f[e] = f[e] * inv * h[e];
+    for (int e = 0; e < NP; ++e) f[e] = __fmul2_rn(__fmul2_rn(f[e], make_float2(inv, inv)), h[e]);
     set(f);
   }
 };
@@ -261,68 +266,105 @@ __device__ __forceinline__ float2 rope_cs(const Rope& r, int pos, int i) {
   sincospif(2.0f * (float)(t - rint(t)), &s, &c);
   return make_float2(c, s);
 }
+__device__ __forceinline__ float2 turn(float2 x, float2 cs) {
+  return make_float2(x.x * cs.x - x.y * cs.y, x.x * cs.y + x.y * cs.x);
+}
 
-// Lanes of one row (G of them, a power of two) add up their squares and return
-// 1 / sqrt(sum / n + eps).  `sum(by)` is a lane's sum of (by x)^2: where the
-// plain sum passes the range of 32 bits it is taken again with by = 2^-64.
-template <class Sum>
-__device__ __forceinline__ float row_rms(Sum sum, int n, float eps, int G) {
-  auto all = [&](float ss) {
+// The threads of one row add up their sums of squares: G neighbouring lanes (a
+// power of two) of a warp in which every lane takes part,
+template <int G>
+struct LaneTotal {
+  __device__ __forceinline__ float operator()(float ss) const {
+#pragma unroll
     for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     return ss;
-  };
-  float ss = all(sum(1.f));
-  if (__any_sync(0xffffffffu, isinf(ss))) {
-    const float small = all(sum(0x1p-64f));
-    if (isinf(ss)) return rsqrtf(small / (float)n + eps * 0x1p-64f * 0x1p-64f) * 0x1p-64f;
   }
-  return rsqrtf(ss / (float)n + eps);
-}
+  __device__ __forceinline__ bool any(bool b) const { return __any_sync(0xffffffffu, b); }
+};
+// or W whole warps, which share named barrier `bar` and two sets of W words of
+// shared memory, used in turn so that one barrier is enough.  Every thread adds
+// the words in the same order.
+template <int W>
+struct WarpsTotal {
+  float* words;
+  int warp, bar;
+  int* flip;
+  __device__ __forceinline__ float operator()(float ss) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    float* const w = words + *flip * W;
+    *flip ^= 1;
+    if ((threadIdx.x & 31) == 0) w[warp] = ss;
+    sm100::named_bar_sync(bar, 32 * W);
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) ss += w[i];
+    return ss;
+  }
+  __device__ __forceinline__ bool any(bool b) const { return b; }  // the same in every thread
+};
 
-// RMS norm of one row of n elements by one warp: out = x rsqrt(mean(x^2) +
-// eps) gamma, in 32 bits and rounded once (a null gamma copies the row).  Up
-// to NV vectors per lane stay in registers; a longer row is read a second
-// time, from L1 or L2.  `x` and `out` may be the same row.
-constexpr int NV = 8;
-template <typename T, bool kVec>
-__device__ __forceinline__ void warp_rms_row(const T* x, const T* gamma, T* out, int n, float eps, int lane) {
+// A thread's share of one row of n elements that `lanes` threads hold, this
+// being number `lane`: NV vectors in registers; what a longer row has besides
+// is read a second time, from L1 or L2.
+template <typename T, bool kVec, int NV>
+struct RowPart {
   using V = Vec<T, kVec>;
-  const int nv = n / V::VE;
-  V v[NV], g[NV];  // gamma is asked for before the sum is known
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (lane + 32 * i < nv) v[i].load(x + (lane + 32 * i) * V::VE);
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (gamma && lane + 32 * i < nv) g[i].load(gamma + (lane + 32 * i) * V::VE);
-  const float inv = row_rms([&](float by) {
-    float ss = 0.f;
+  V v[NV];
+  __device__ __forceinline__ void load(const T* x, int nv, int lane, int lanes) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (lane + 32 * i < nv) v[i].squares(ss, by);
-    for (int i = lane + 32 * NV; i < nv; i += 32) {
+      if (lane + lanes * i < nv) v[i].load(x + (lane + lanes * i) * V::VE);
+  }
+  template <bool kScaled>
+  __device__ __forceinline__ float squares(const T* x, int nv, int lane, int lanes, float by) const {
+    float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane + lanes * i < nv) v[i].template squares<kScaled>(ss, by);
+    for (int i = lane + lanes * NV; i < nv; i += lanes) {
       V u;
       u.load(x + i * V::VE);
-      u.squares(ss, by);
+      u.template squares<kScaled>(ss, by);
     }
-    return ss;
-  }, n, eps, 32);
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (lane + 32 * i < nv) {
-      if (gamma) v[i].norm(inv, g[i]);
-      v[i].store(out + (lane + 32 * i) * V::VE);
-    }
-  for (int i = lane + 32 * NV; i < nv; i += 32) {
-    V u, w;
-    u.load(x + i * V::VE);
-    if (gamma) {
-      w.load(gamma + i * V::VE);
-      u.norm(inv, w);
-    }
-    u.store(out + i * V::VE);
+    return ss.x + ss.y;
   }
-}
+  // RMS norm: out = x / sqrt(mean(x^2) + eps) * gamma in 32 bits, rounded once;
+  // a null gamma copies the row.  `x` and `out` may be the same row; `g` is
+  // this thread's share of gamma.  Where the sum of squares passes the range
+  // of 32 bits it is taken again of x 2^-64.  `live` is false in threads that
+  // only take part in the sums.
+  template <class Total>
+  __device__ __forceinline__ void norm(const RowPart& g, const T* x, const T* gamma, T* out, int nv, float inv_n,
+                                       float eps, int lane, int lanes, bool live, const Total& total) {
+    float inv = 1.f;
+    if (gamma) {  // the same for every row
+      const int own = live ? nv : 0;
+      const float ss = total(squares<false>(x, own, lane, lanes, 1.f));
+      inv = rsqrtf(fmaf(ss, inv_n, eps));
+      if (total.any(isinf(ss))) {
+        const float small = total(squares<true>(x, own, lane, lanes, 0x1p-64f));
+        if (isinf(ss)) inv = rsqrtf(fmaf(small, inv_n, eps * 0x1p-64f * 0x1p-64f)) * 0x1p-64f;
+      }
+    }
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane + lanes * i < nv) {
+        if (gamma) v[i].norm(inv, g.v[i]);
+        v[i].store(out + (lane + lanes * i) * V::VE);
+      }
+    for (int i = lane + lanes * NV; i < nv; i += lanes) {
+      V u, w;
+      u.load(x + i * V::VE);
+      if (gamma) {
+        w.load(gamma + i * V::VE);
+        u.norm(inv, w);
+      }
+      u.store(out + i * V::VE);
+    }
+  }
+};
 
 // The two adjacent elements of a pair: one load or store in the vector form.
 template <typename T, bool kVec>
@@ -332,20 +374,22 @@ __device__ __forceinline__ float2 load_pair(const T* p) {
   else return *reinterpret_cast<const float2*>(p);
 }
 template <typename T, bool kVec>
-__device__ __forceinline__ void put_pair(T* p, float a, float b) {
+__device__ __forceinline__ void put_pair(T* p, float2 v) {
   if constexpr (kVec) {
-    store_pair(p, a, b);
+    store_pair(p, v.x, v.y);
   } else {
-    p[0] = from_f32<T>(a);
-    p[1] = from_f32<T>(b);
+    p[0] = from_f32<T>(v.x);
+    p[1] = from_f32<T>(v.y);
   }
 }
 
 // --------------------------------------------------- normalised append
-// One warp per row and latent: warps of even index take the cache row
-// [rms(c) gamma | RoPE(k_R)], the others c_Q (when there is one).  Each
-// element is read and written once, so it is bound by memory (by latency at
-// decode sizes); a warp's whole row is in flight at once.
+// With a query latent, a block per row: warp 0 takes the cache row
+// [rms(c) gamma | RoPE(k_R)], the other three c_Q, which is about three times as
+// long, so that every thread moves two to four vectors.  Without one, a warp per
+// row.  Each element is read and written once: bound by memory, by latency at
+// decode sizes.  So a warp walks several rows where there are many, keeps its
+// share of gamma, and asks for the next row before it works on this one.
 struct NormAppendArgs {
   const void* kv;        // [T][kv_stride]: [c (d_c) | k_R]
   const void* kv_gamma;  // [d_c] or null
@@ -363,46 +407,86 @@ struct NormAppendArgs {
 };
 constexpr int NORM_THREADS = 128;
 
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(NORM_THREADS) norm_append_kernel(const NormAppendArgs a) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * (NORM_THREADS / 32) + (threadIdx.x >> 5);
-  const int parts = a.cq ? 2 : 1;
-  const long long t = w / parts;
-  if (t >= a.T) return;
-  if (w - t * parts == 1) {
-    warp_rms_row<T, kVec>(static_cast<const T*>(a.cq) + t * a.cq_stride, static_cast<const T*>(a.cq_gamma),
-                          static_cast<T*>(a.cq_out) + t * a.cq_out_stride, a.d_cq, a.eps, lane);
+template <typename T, bool kVec, int NV>
+__global__ void __launch_bounds__(NORM_THREADS, NV == 2 ? 8 : 4) norm_append_kernel(const NormAppendArgs a) {
+  using Part = RowPart<T, kVec, NV>;
+  constexpr int VE = Vec<T, kVec>::VE;
+  __shared__ float words[6];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (a.cq && warp > 0) {
+    const int i = threadIdx.x - 32, nv = a.d_cq / VE;
+    const T* const gamma = static_cast<const T*>(a.cq_gamma);
+    const float inv_n = 1.f / (float)a.d_cq;
+    int flip = 0;
+    const WarpsTotal<3> total{words, warp - 1, 1, &flip};
+    auto row = [&](int t) { return static_cast<const T*>(a.cq) + t * a.cq_stride; };
+    Part cur, nxt, g;
+    int t = blockIdx.x;
+    if (t < a.T) cur.load(row(t), nv, i, 96);
+    if (gamma) g.load(gamma, nv, i, 96);
+    for (; t < a.T; t += gridDim.x) {
+      if (t + (int)gridDim.x < a.T) nxt.load(row(t + gridDim.x), nv, i, 96);
+      cur.norm(g, row(t), gamma, static_cast<T*>(a.cq_out) + t * a.cq_out_stride, nv, inv_n, a.eps, i, 96, true, total);
+      cur = nxt;
+    }
     return;
   }
-  const long long slot = a.slot[t];
-  if (slot < 0 || slot >= a.num_slots) {
-    if (slot != -1 && lane == 0) flag_error(a.err, kErrBounds);
-    return;
-  }
-  const T* const x = static_cast<const T*>(a.kv) + t * a.kv_stride;
-  T* const row = static_cast<T*>(a.cache) + slot * a.d_cr;
-  const int pos = a.pos[t], half = a.rope.half, pairs = (a.d_cr - a.d_c) / 2;
-  float2 k = make_float2(0.f, 0.f);  // the shared key is at most one pair per lane
-  if (lane < pairs) k = load_pair<T, kVec>(x + a.d_c + 2 * lane);
-  const float2 cs = lane < half ? rope_cs(a.rope, pos, lane) : make_float2(1.f, 0.f);
-  warp_rms_row<T, kVec>(x, static_cast<const T*>(a.kv_gamma), row, a.d_c, a.eps, lane);
-  for (int i = lane;; i += 32) {
-    // With a key per head, pair i belongs to head i / half; its angle's sine and cosine sit in lane i % half.
-    const int own = i % half;
-    const float c = __shfl_sync(0xffffffffu, cs.x, own), s = __shfl_sync(0xffffffffu, cs.y, own);
-    if (i < pairs) put_pair<T, kVec>(row + a.d_c + 2 * i, k.x * c - k.y * s, k.x * s + k.y * c);
-    if (i - lane + 32 >= pairs) break;  // the same in every lane
-    if (i + 32 < pairs) k = load_pair<T, kVec>(x + a.d_c + 2 * (i + 32));
+  const int step = a.cq ? gridDim.x : gridDim.x * (NORM_THREADS / 32);
+  const int nv = a.d_c / VE, half = a.rope.half, pairs = (a.d_cr - a.d_c) / 2;
+  const T* const gamma = static_cast<const T*>(a.kv_gamma);
+  const float inv_n = 1.f / (float)a.d_c;
+  struct Row {
+    Part c;
+    float2 k;  // the shared key is at most one pair per lane
+    long long slot;
+    int pos;
+  };
+  auto src = [&](int t) { return static_cast<const T*>(a.kv) + t * a.kv_stride; };
+  auto load = [&](Row& r, int t) {
+    const T* const x = src(t);
+    r.c.load(x, nv, lane, 32);
+    if (lane < pairs) r.k = load_pair<T, kVec>(x + a.d_c + 2 * lane);
+    r.slot = a.slot[t];
+    r.pos = a.pos[t];
+  };
+  Row cur, nxt;
+  Part g;
+  int t = a.cq ? blockIdx.x : blockIdx.x * (NORM_THREADS / 32) + warp;
+  if (t < a.T) load(cur, t);
+  if (gamma) g.load(gamma, nv, lane, 32);
+  for (; t < a.T; t += step) {
+    if (t < a.T - step) load(nxt, t + step);
+    if (cur.slot >= 0 && cur.slot < a.num_slots) {
+      T* const dst = static_cast<T*>(a.cache) + cur.slot * a.d_cr;
+      const float2 cs = lane < half ? rope_cs(a.rope, cur.pos, lane) : make_float2(1.f, 0.f);
+      cur.c.norm(g, src(t), gamma, dst, nv, inv_n, a.eps, lane, 32, true, LaneTotal<32>{});
+      if (pairs == half) {
+        if (lane < pairs) put_pair<T, kVec>(dst + a.d_c + 2 * lane, turn(cur.k, cs));
+      } else {
+        // A key per head: pair i belongs to head i / half, and its angle's sine and cosine sit in lane i % half.
+        for (int i0 = 0; i0 < pairs; i0 += 32) {
+          const int i = i0 + lane, own = i % half;
+          const float2 c = make_float2(__shfl_sync(0xffffffffu, cs.x, own), __shfl_sync(0xffffffffu, cs.y, own));
+          if (i0 > 0 && i < pairs) cur.k = load_pair<T, kVec>(src(t) + a.d_c + 2 * i);
+          if (i < pairs) put_pair<T, kVec>(dst + a.d_c + 2 * i, turn(cur.k, c));
+        }
+      }
+    } else if (cur.slot != -1 && lane == 0) {
+      flag_error(a.err, kErrBounds);
+    }
+    cur = nxt;
   }
 }
 
 // --------------------------------------------------- query norm, rotation
-// A block takes `hpb` heads of one token.  A head's content is normalised by a
-// group of G lanes (the power of two that holds it as 16-byte vectors, so a
-// warp works on 32 / G heads at once); the position parts of a block's heads
-// share one table of sines and cosines and are walked as one array.  Bound by
-// memory: every element is read and written once.
+// A block takes some heads of one token.  A head's content is normalised by a
+// group of G lanes (the power of two that holds it as 16-byte vectors, VPL of
+// them per lane), two heads per group in a step; the position parts of a step's
+// heads are turned by groups of 2^rope_shift lanes, so that a thread turns the
+// same pairs of every head and keeps their sines and cosines, as it keeps its
+// share of gamma.  Every element is read and written once.  What bounded the
+// first versions was occupancy (two blocks an SM), then issued instructions
+// (divisions by the group's size, one value at a time).
 struct QueryArgs {
   const void* q;       // [T][n_h] rows [q_C (d_h) | q_R (d_r)], q_stride per token
   const void* gamma;   // [d_h] or null
@@ -410,98 +494,82 @@ struct QueryArgs {
   void* qr;            // position part out
   const int32_t* pos;
   long long q_stride, qc_ts, qc_hs, qr_ts, qr_hs;
-  int T, n_h, d_h, d_r, hpb, group;
+  int T, n_h, d_h, d_r, hpb, rope_shift;  // hpb: heads per block, a multiple of a step's
   float eps;
   Rope rope;
 };
-constexpr int QUERY_THREADS = 256;
-constexpr int QNV = 4;  // vectors of a head's content that a lane keeps
+constexpr int QUERY_THREADS = 128;
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, int G, int VPL>
 __global__ void __launch_bounds__(QUERY_THREADS) query_norm_rope_kernel(const QueryArgs a) {
   using V = Vec<T, kVec>;
+  using Part = RowPart<T, kVec, VPL>;
+  constexpr int PER = QUERY_THREADS / G, STEP = 2 * PER;  // heads at a time and per step
+  constexpr int PE = kVec ? V::VE : 2;                    // position parts: vectors of whole pairs, or single pairs
   __shared__ float2 cs[32];
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, sub = tid & (G - 1), grp = tid / G;
   const long long t = blockIdx.x;
+  const int nv = a.d_h / V::VE, dq = a.d_h + a.d_r;
   const int h0 = blockIdx.y * a.hpb, h1 = min(a.n_h, h0 + a.hpb);
-  const int dq = a.d_h + a.d_r, G = a.group, sub = lane & (G - 1);
+  const int e0 = (tid & ((1 << a.rope_shift) - 1)) * PE, rgrp = tid >> a.rope_shift, rper = QUERY_THREADS >> a.rope_shift;
+  const bool turns = e0 < a.d_r;
   const T* const x = static_cast<const T*>(a.q) + t * a.q_stride;
   const T* const gamma = static_cast<const T*>(a.gamma);
-  if (tid < a.rope.half) cs[tid] = rope_cs(a.rope, a.pos[t], tid);
+  const float inv_n = 1.f / (float)a.d_h;
 
-  const int nv = a.d_h / V::VE;
-  V g[QNV];
+  struct Work {
+    Part c[2];
+    V r;         // the thread's first position part of the step
+    float2 pair; // the same without vectors
+  };
+  auto load_turn = [&](Work& w, int h) {
+    const T* const p = x + (long long)h * dq + a.d_h + e0;
+    if constexpr (kVec) w.r.load(p);
+    else w.pair = load_pair<T, false>(p);
+  };
+  auto load = [&](Work& w, int hb) {
 #pragma unroll
-  for (int i = 0; i < QNV; ++i)
-    if (gamma && sub + G * i < nv) g[i].load(gamma + (sub + G * i) * V::VE);
-  const int per = QUERY_THREADS / G;  // heads at a time
-  for (int hb = h0; hb < h1; hb += per) {
-    const int h = hb + tid / G;
-    const bool live = h < h1;
-    const T* const xc = x + (long long)h * dq;
-    T* const out = static_cast<T*>(a.qc) + t * a.qc_ts + h * a.qc_hs;
-    V v[QNV];
-#pragma unroll
-    for (int i = 0; i < QNV; ++i)
-      if (live && sub + G * i < nv) v[i].load(xc + (sub + G * i) * V::VE);
-    const float inv = row_rms([&](float by) {
-      float ss = 0.f;
-      if (!live) return ss;
-#pragma unroll
-      for (int i = 0; i < QNV; ++i)
-        if (sub + G * i < nv) v[i].squares(ss, by);
-      for (int i = sub + G * QNV; i < nv; i += G) {
-        V u;
-        u.load(xc + i * V::VE);
-        u.squares(ss, by);
-      }
-      return ss;
-    }, a.d_h, a.eps, G);
-    if (!live) continue;
-#pragma unroll
-    for (int i = 0; i < QNV; ++i)
-      if (sub + G * i < nv) {
-        if (gamma) v[i].norm(inv, g[i]);
-        v[i].store(out + (sub + G * i) * V::VE);
-      }
-    for (int i = sub + G * QNV; i < nv; i += G) {
-      V u, w;
-      u.load(xc + i * V::VE);
-      if (gamma) {
-        w.load(gamma + i * V::VE);
-        u.norm(inv, w);
-      }
-      u.store(out + i * V::VE);
+    for (int i = 0; i < 2; ++i) {
+      const int h = hb + i * PER + grp;
+      if (h < h1) w.c[i].load(x + (long long)h * dq, nv, sub, G);
     }
-  }
+    if (turns && hb + rgrp < min(h1, hb + STEP)) load_turn(w, hb + rgrp);
+  };
+  Work cur, nxt;
+  load(cur, h0);
+  Part g;
+  if (gamma) g.load(gamma, nv, sub, G);
+  if (tid < a.rope.half) cs[tid] = rope_cs(a.rope, a.pos[t], tid);
   __syncthreads();
-  // Position parts: vectors of whole pairs (single pairs without them).
-  constexpr int PE = kVec ? V::VE : 2;
-  const int nr = a.d_r / PE, total = (h1 - h0) * nr;
-  for (int i = tid; i < total; i += QUERY_THREADS) {
-    const int h = h0 + i / nr, e0 = (i % nr) * PE;
-    const T* const xr = x + (long long)h * dq + a.d_h + e0;
-    T* const out = static_cast<T*>(a.qr) + t * a.qr_ts + h * a.qr_hs + e0;
-    if constexpr (kVec) {
-      V v;
-      float f[V::VE];
-      v.load(xr);
-      v.get(f);
+  float2 c[PE / 2];
 #pragma unroll
-      for (int e = 0; e < V::VE; e += 2) {
-        const float2 c = cs[(e0 + e) >> 1];
-        const float x0 = f[e], x1 = f[e + 1];
-        f[e] = x0 * c.x - x1 * c.y;
-        f[e + 1] = x0 * c.y + x1 * c.x;
-      }
-      v.set(f);
-      v.store(out);
-    } else {
-      const float2 c = cs[e0 >> 1];
-      const float x0 = to_f32(xr[0]), x1 = to_f32(xr[1]);
-      out[0] = from_f32<T>(x0 * c.x - x1 * c.y);
-      out[1] = from_f32<T>(x0 * c.y + x1 * c.x);
+  for (int i = 0; i < PE / 2; ++i) c[i] = turns ? cs[e0 / 2 + i] : make_float2(1.f, 0.f);
+
+  for (int hb = h0; hb < h1; hb += STEP) {
+    if (hb + STEP < h1) load(nxt, hb + STEP);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int h = hb + i * PER + grp;
+      cur.c[i].norm(g, x + (long long)h * dq, gamma, static_cast<T*>(a.qc) + t * a.qc_ts + h * a.qc_hs, nv, inv_n, a.eps,
+                    sub, G, h < h1, LaneTotal<G>{});
     }
+    const int he = min(h1, hb + STEP);
+    if (turns)
+      for (int h = hb + rgrp; h < he; h += rper) {
+        if (h != hb + rgrp) load_turn(cur, h);
+        T* const out = static_cast<T*>(a.qr) + t * a.qr_ts + h * a.qr_hs + e0;
+        if constexpr (kVec) {
+          float2 f[V::NP];
+          cur.r.get(f);
+#pragma unroll
+          for (int i = 0; i < V::NP; ++i) f[i] = turn(f[i], c[i]);
+          cur.r.set(f);
+          cur.r.store(out);
+        } else {
+          put_pair<T, false>(out, turn(cur.pair, c[0]));
+        }
+      }
+    cur = nxt;
   }
 }
 

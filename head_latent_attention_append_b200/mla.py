@@ -260,36 +260,24 @@ def decode_cp_combine(w: Weights, obar_parts, lse_parts, out, workspace, stream=
 
 
 # ---------------------------------------------------------------- ragged step
-# These calls check their tensors: sizes are taken from the shapes, so a wrong
-# shape, type or device would reach memory that is not the caller's.
-def _checked(fn: str, device, tensors):
-    """Each (name, tensor, dtype, shape, packed): on `device`, of that type and shape (None: any size); with
-    `packed` contiguous, else with a contiguous last axis."""
-    for name, t, dtype, shape, packed in tensors:
-        if t.dtype != dtype:
-            raise MlaError(fn, -1, f"{name}: {t.dtype}, expected {dtype}")
-        if t.device != device:
-            raise MlaError(fn, -1, f"{name} is on {t.device}, expected {device}")
-        got = t.shape
-        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
-            raise MlaError(fn, -1, f"{name}: shape {tuple(got)}, expected {tuple('any' if w is None else w for w in shape)}")
-        if not (t.is_contiguous() if packed else (t.stride(-1) == 1 or got[-1] <= 1)):
-            raise MlaError(fn, -1, f"{name}: not contiguous" + ("" if packed else " along the last axis"))
+# These calls go through a compiled module, which checks every tensor's type,
+# device, shape and layout (sizes are taken from the shapes) and calls libmla:
+# in Python that costs several times what the kernels take at decode sizes.  It
+# answers 1, without having called libmla, when a tensor is not the call's; the
+# checks below then find the one to name.
+_ragged = None
 
 
-def _on(fn: str, device, stream):
-    """The raw stream for tensors of `device`, which has to be the current device."""
-    import torch
-    if device.type != "cuda":
-        raise MlaError(fn, -1, f"tensors are on {device}, expected a CUDA device")
-    if device.index != torch.cuda.current_device():
-        raise MlaError(fn, -1, f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
-
-
-def _step_of(t, axis: int, least: int) -> int:
-    """The stride of an axis; of one with a single entry, any will do."""
-    return t.stride(axis) if t.shape[axis] > 1 else least
+def _module():
+    global _ragged
+    if _ragged is None:
+        import torch  # noqa: F401  (its libraries, which the module is linked to)
+        try:
+            from . import _ragged as m
+        except ImportError as e:
+            raise ImportError(f"_ragged.so cannot be loaded ({e}); run head_latent_attention_append_b200/build.py") from e
+        _ragged = m
+    return _ragged
 
 
 def _path_dtype(dims: Dims):
@@ -297,69 +285,80 @@ def _path_dtype(dims: Dims):
     return torch.bfloat16 if dims.dtype == BF16 else torch.float32
 
 
+def _refuse(fn: str, code: int, tensors):
+    """Raises for a call that answered `code`.  Each tensor: (name, tensor or None, dtype, shape (None: any size),
+    packed: contiguous, else with a contiguous last axis); the first one gives the device."""
+    import torch
+    if code != 1:
+        raise MlaError(fn, code)
+    device = None
+    for name, t, dtype, shape, packed in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise MlaError(fn, -1, f"{name}: a tensor is expected")
+        device = t.device if device is None else device
+        got = tuple(t.shape)
+        if t.dtype != dtype:
+            raise MlaError(fn, -1, f"{name}: {t.dtype}, expected {dtype}")
+        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+            raise MlaError(fn, -1, f"{name}: shape {got}, expected {tuple('any' if w is None else w for w in shape)}")
+        if t.device != device:
+            raise MlaError(fn, -1, f"{name} is on {t.device}, expected {device}")
+        if not (t.is_contiguous() if packed else (t.stride(-1) == 1 or got[-1] <= 1)):
+            raise MlaError(fn, -1, f"{name}: not contiguous" + ("" if packed else " along the last axis"))
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise MlaError(fn, -1, f"tensors are on {device}, expected the current CUDA device")
+    raise MlaError(fn, -1, "an argument is missing or of another kind")
+
+
 def plan_step(new_len, past_len, free_pages, page_table, num_pages: int, q_start, kv_len, seq_idx, pos, slot, counts,
               device_error=None, stream=None):
     """Page-table entries, slots and positions of a ragged step from the requests' lengths (include/mla.h)."""
-    import torch
-    fn, i32, dev = "mla_plan_step", torch.int32, new_len.device
-    B, rows = new_len.shape[0], seq_idx.shape[0]
-    _checked(fn, dev, (("new_len", new_len, i32, (B,), True), ("past_len", past_len, i32, (B,), True),
-                       ("free_pages", free_pages, i32, (None,), True), ("page_table", page_table, i32, (B, None), True),
-                       ("q_start", q_start, i32, (B + 1,), True), ("kv_len", kv_len, i32, (B,), True),
-                       ("seq_idx", seq_idx, i32, (rows,), True), ("pos", pos, i32, (rows,), True),
-                       ("slot", slot, torch.int64, (rows,), True), ("counts", counts, i32, (3,), True)))
-    if device_error is not None:
-        _checked(fn, dev, (("device_error", device_error, i32, (1,), True),))
-    st = _on(fn, dev, stream)
-    _check(fn, lib.mla_plan_step(
-        new_len.data_ptr(), past_len.data_ptr(), B, free_pages.data_ptr(), free_pages.shape[0], page_table.data_ptr(),
-        page_table.shape[1], num_pages, q_start.data_ptr(), kv_len.data_ptr(), seq_idx.data_ptr(), pos.data_ptr(),
-        slot.data_ptr(), rows, counts.data_ptr(), _ptr(device_error), st))
+    s = (_ragged or _module()).plan_step(new_len, past_len, free_pages, page_table, num_pages, q_start, kv_len, seq_idx,
+                                         pos, slot, counts, device_error, stream)
+    if s:
+        import torch
+        i32, B, rows = torch.int32, new_len.shape[0], seq_idx.shape[0]
+        _refuse("mla_plan_step", s, (
+            ("new_len", new_len, i32, (B,), True), ("past_len", past_len, i32, (B,), True),
+            ("free_pages", free_pages, i32, (None,), True), ("page_table", page_table, i32, (B, None), True),
+            ("q_start", q_start, i32, (B + 1,), True), ("kv_len", kv_len, i32, (B,), True),
+            ("seq_idx", seq_idx, i32, (rows,), True), ("pos", pos, i32, (rows,), True),
+            ("slot", slot, torch.int64, (rows,), True), ("counts", counts, i32, (3,), True),
+            ("device_error", device_error, i32, (1,), True)))
 
 
 def append_normed(dims: Dims, kv, kv_gamma, pos, slot, cache, eps: float = 1e-6, cq=None, cq_gamma=None, cq_out=None,
                   device_error=None, stream=None):
     """RMS norms of the latents, rotation of the position key and the write into the paged cache (include/mla.h)."""
-    import torch
-    fn, dt, dev = "mla_append_normed", _path_dtype(dims), kv.device
-    T, d_cr = kv.shape[0], dims.d_c + (dims.n_h if dims.rope_key_per_head else 1) * dims.d_r
-    _checked(fn, dev, (("kv", kv, dt, (T, d_cr), False), ("pos", pos, torch.int32, (T,), True),
-                       ("slot", slot, torch.int64, (T,), True),
-                       ("cache", cache, dt, (None, dims.page_size, d_cr), True)))
-    if kv_gamma is not None:
-        _checked(fn, dev, (("kv_gamma", kv_gamma, dt, (dims.d_c,), True),))
-    cs = os_ = 0
-    if cq is not None or cq_out is not None:
-        if cq is None or cq_out is None:
-            raise MlaError(fn, -1, "cq and cq_out go together")
-        _checked(fn, dev, (("cq", cq, dt, (T, dims.d_cq), False), ("cq_out", cq_out, dt, (T, dims.d_cq), False)))
-        cs, os_ = _step_of(cq, 0, dims.d_cq), _step_of(cq_out, 0, dims.d_cq)
-    if cq_gamma is not None:
-        _checked(fn, dev, (("cq_gamma", cq_gamma, dt, (dims.d_cq,), True),))
-    if device_error is not None:
-        _checked(fn, dev, (("device_error", device_error, torch.int32, (1,), True),))
-    st = _on(fn, dev, stream)
-    _check(fn, lib.mla_append_normed(
-        dims, kv.data_ptr(), _step_of(kv, 0, d_cr), _ptr(kv_gamma), _ptr(cq), cs, _ptr(cq_gamma), _ptr(cq_out), os_, eps,
-        pos.data_ptr(), slot.data_ptr(), cache.data_ptr(), cache.shape[0], T, _ptr(device_error), st))
+    s = (_ragged or _module()).append_normed(dims, kv, kv_gamma, pos, slot, cache, eps, cq, cq_gamma, cq_out,
+                                             device_error, stream)
+    if s:
+        import torch
+        dt, T, row = _path_dtype(dims), kv.shape[0], dims.d_c + (dims.n_h if dims.rope_key_per_head else 1) * dims.d_r
+        if (cq is None) != (cq_out is None):
+            raise MlaError("mla_append_normed", -1, "cq and cq_out go together")
+        _refuse("mla_append_normed", s, (
+            ("kv", kv, dt, (T, row), False), ("kv_gamma", kv_gamma, dt, (dims.d_c,), True),
+            ("pos", pos, torch.int32, (T,), True), ("slot", slot, torch.int64, (T,), True),
+            ("cache", cache, dt, (None, dims.page_size, row), True), ("cq", cq, dt, (T, dims.d_cq), False),
+            ("cq_gamma", cq_gamma, dt, (dims.d_cq,), True), ("cq_out", cq_out, dt, (T, dims.d_cq), False),
+            ("device_error", device_error, torch.int32, (1,), True)))
 
 
 def query_norm_rope(dims: Dims, q, gamma, pos, qc_out, qr_out, eps: float = 1e-6, stream=None):
     """RMS norm of every query head's content and rotation of its position part (include/mla.h)."""
-    import torch
-    fn, dt, dev = "mla_query_norm_rope", _path_dtype(dims), q.device
-    T, n_h, d_h, d_r = q.shape[0], dims.n_h, dims.d_h, dims.d_r
-    _checked(fn, dev, (("q", q, dt, (T, n_h, d_h + d_r), False), ("pos", pos, torch.int32, (T,), True),
-                       ("qc_out", qc_out, dt, (T, n_h, d_h), False), ("qr_out", qr_out, dt, (T, n_h, d_r), False)))
-    if n_h > 1 and q.stride(1) != d_h + d_r:
-        raise MlaError(fn, -1, "q: a token's heads have to be contiguous")
-    if gamma is not None:
-        _checked(fn, dev, (("gamma", gamma, dt, (d_h,), True),))
-    st = _on(fn, dev, stream)
-    ch, rh = _step_of(qc_out, 1, d_h), _step_of(qr_out, 1, d_r)
-    _check(fn, lib.mla_query_norm_rope(
-        dims, q.data_ptr(), _step_of(q, 0, n_h * (d_h + d_r)), _ptr(gamma), eps, pos.data_ptr(), qc_out.data_ptr(),
-        _step_of(qc_out, 0, n_h * ch), ch, qr_out.data_ptr(), _step_of(qr_out, 0, n_h * rh), rh, T, st))
+    s = (_ragged or _module()).query_norm_rope(dims, q, gamma, pos, qc_out, qr_out, eps, stream)
+    if s:
+        import torch
+        dt, T, n_h, d_h, d_r = _path_dtype(dims), q.shape[0], dims.n_h, dims.d_h, dims.d_r
+        if s == 1 and q.dim() == 3 and n_h > 1 and q.shape[1:] == (n_h, d_h + d_r) and q.stride(1) != d_h + d_r:
+            raise MlaError("mla_query_norm_rope", -1, "q: a token's heads have to be contiguous")
+        _refuse("mla_query_norm_rope", s, (
+            ("q", q, dt, (T, n_h, d_h + d_r), False), ("gamma", gamma, dt, (d_h,), True),
+            ("pos", pos, torch.int32, (T,), True), ("qc_out", qc_out, dt, (T, n_h, d_h), False),
+            ("qr_out", qr_out, dt, (T, n_h, d_r), False)))
 
 
 def attend_ragged_workspace_bytes(dims: Dims, B: int, T: int) -> int:
@@ -368,23 +367,16 @@ def attend_ragged_workspace_bytes(dims: Dims, B: int, T: int) -> int:
 
 def attend_ragged(dims: Dims, q, q_start, kv_len, page_table, cache, out, lse, workspace, stream=None):
     """Absorbed attention of every request's new tokens over its paged cache (include/mla.h)."""
-    import torch
-    fn, dt, i32, dev = "mla_attend_ragged", _path_dtype(dims), torch.int32, q.device
-    T, B, n_h, d_cr = q.shape[0], kv_len.shape[0], dims.n_h, dims.d_c + dims.d_r
-    _checked(fn, dev, (("q", q, dt, (T, n_h, d_cr), False), ("q_start", q_start, i32, (B + 1,), True),
-                       ("kv_len", kv_len, i32, (B,), True), ("page_table", page_table, i32, (B, None), True),
-                       ("cache", cache, dt, (None, dims.page_size, d_cr), True),
-                       ("out", out, dt, (T, n_h, dims.d_c), True)))
-    if lse is not None:
-        _checked(fn, dev, (("lse", lse, torch.float32, (T, n_h), True),))
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise MlaError(fn, -1, f"workspace: contiguous memory on {dev} expected")
-    st = _on(fn, dev, stream)
-    hs = _step_of(q, 1, d_cr)
-    _check(fn, lib.mla_attend_ragged(
-        dims, q.data_ptr(), _step_of(q, 0, n_h * hs), hs, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
-        page_table.shape[1], cache.shape[0], cache.data_ptr(), out.data_ptr(), _ptr(lse), B, T, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), st))
+    s = (_ragged or _module()).attend_ragged(dims, q, q_start, kv_len, page_table, cache, out, lse, workspace, stream)
+    if s:
+        import torch
+        dt, i32, T, B, n_h, row = _path_dtype(dims), torch.int32, q.shape[0], kv_len.shape[0], dims.n_h, dims.d_c + dims.d_r
+        _refuse("mla_attend_ragged", s, (
+            ("q", q, dt, (T, n_h, row), False), ("q_start", q_start, i32, (B + 1,), True),
+            ("kv_len", kv_len, i32, (B,), True), ("page_table", page_table, i32, (B, None), True),
+            ("cache", cache, dt, (None, dims.page_size, row), True), ("out", out, dt, (T, n_h, dims.d_c), True),
+            ("lse", lse, torch.float32, (T, n_h), True),
+            ("workspace", workspace, workspace.dtype, tuple(workspace.shape), True)))
 
 
 def selftest_wait_timeout(workspace, limit_us: int, stream=None):
