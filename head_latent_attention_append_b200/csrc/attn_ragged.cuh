@@ -434,23 +434,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     };
 
     uint32_t j = 0, part_par = 0;  // bit s: parity of the next edge load in latent slot s
-    RSeg g_cur = seg_lo < seg_hi ? segs[seg_lo] : RSeg{};
-    RSeg g_nxt = seg_lo + 1 < seg_hi ? segs[seg_lo + 1] : g_cur;
+    // The page loop keeps four numbers of its segment; the rest is read again at
+    // its ends (three segments in registers were 4% slower, a ring of them in
+    // shared memory 2%).
     if (seg_lo < seg_hi) {  // every softmax thread: q_store holds named barriers
-      q_issue(g_cur);
+      q_issue(segs[seg_lo]);
       q_store();
     }
     for (int si = seg_lo; si < seg_hi; ++si) {
-      const RSeg g = g_cur;
-      const int n = g.t_hi - g.t_lo;
-      // Keys that this thread's row sees (none for a row past the block's).
-      const int lim = my_row < g.nrows ? min(max(g.base + (g.row0 + my_row) / a.n_h + 1, 0), g.nkeys) : 0;
+      int t_lo, n, kmin, lim;
+      {
+        const RSeg g = segs[si];
+        t_lo = g.t_lo;
+        n = g.t_hi - g.t_lo;
+        kmin = g.kmin;
+        // Keys that this thread's row sees (none for a row past the block's).
+        lim = my_row < g.nrows ? min(max(g.base + (g.row0 + my_row) / a.n_h + 1, 0), g.nkeys) : 0;
+      }
       float m_used = -INFINITY, lt = 0.f;  // in base 2; O and the sums are relative to ref_max(m_used)
       for (int i = 0; i < n; ++i, ++j) {
-        const int t = g.t_lo + i;
+        const int t = t_lo + i;
         const uint32_t b = j & 1;
-        const bool q_next = i + 1 == n && si + 1 < seg_hi;
-        if (si + 1 < seg_hi && i == max(0, n - 6)) prefetch_q(g_nxt);
+        const bool edge = (t + 1) * KT > kmin;  // edge_page
+        if (si + 1 < seg_hi && i == max(0, n - 6)) prefetch_q(segs[si + 1]);
         // S of page j is complete, and with it every earlier MMA: P*V of page
         // j - 2 (issued before S(j)) has released P tile b.
         ok = ok && wait_all(&s_full[b], (j >> 1) & 1);
@@ -467,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int x = 0; x < 16; ++x) s[x] = 0.f;
         }
         const int k0 = kh * 32 + ch * 16;  // this thread's first key of the page
-        if (edge_page(g, t)) {
+        if (edge) {
           const int rel = lim - t * KT - k0;
 #pragma unroll
           for (int x = 0; x < 16; ++x)
@@ -538,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           *reinterpret_cast<uint4*>(prow + ((u0 ^ (hl & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           *reinterpret_cast<uint4*>(prow + (((u0 + 1) ^ (hl & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
         }
-        if (ok && edge_page(g, t)) {
+        if (ok && edge) {
           // 0 * NaN would poison O: rows behind the block's last key are
           // cleared, and in rows that only some of the block's rows see the
           // infinities and NaNs are (see the head of this file).
@@ -547,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           part_par ^= 1u << vs;
           if (ok) {
             uint8_t* vb = smem + OFF_VG + vs * VG_BYTES;
-            const int first = max(0, g.kmin - t * KT), gone = min(KT, max(0, g.nkeys - t * KT));
+            const int first = max(0, kmin - t * KT), gone = min(KT, max(0, segs[si].nkeys - t * KT));
             const int rows = KT - first, units = rows * 8 * NPV;
             for (int x = tid - 128; x < units; x += 256) {
               const int qq = x / (rows * 8), rem = x - qq * rows * 8, r = first + rem / 8;
@@ -577,10 +583,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // ---- end of the segment ----
         // The next segment's Q replaces this one's (its last score MMA is
         // complete); then O of this segment, once its last P*V is done.
-        if (q_next) {  // every softmax thread: q_store holds named barriers
-          q_issue(g_nxt);
+        if (si + 1 < seg_hi) {  // every softmax thread: q_store holds named barriers
+          q_issue(segs[si + 1]);
           q_store();
         }
+        const RSeg g = segs[si];
         ok = ok && wait_all(&pv_done[b], (j >> 1) & 1);
         lsum[hl * 4 + part] = lt;
         named_bar_sync(1 + grp, 128);
@@ -655,8 +662,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           signal_even(o_free_even);
         }
       }
-      g_cur = g_nxt;
-      if (si + 2 < seg_hi) g_nxt = segs[si + 2];
     }
   }
 

@@ -131,8 +131,8 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
                             tc ? kBlockTilesTc : kBlockTilesSimt, S, err, ints};
     if ((e = set_smem_once(ragged_sched_kernel, sizeof(int) * (size_t)kRaggedSmemInts))) return cuda_status(e);
     ++g_launches;
-    ragged_sched_kernel<<<1, P.r_max > 1024 ? 1024 : 256, sizeof(int) * (size_t)ints, st>>>(a);
-    if ((e = cudaGetLastError())) return cuda_status(e);
+    if ((e = launch_pdl(ragged_sched_kernel, dim3(1), dim3(P.r_max > 1024 ? 1024 : 256), sizeof(int) * (size_t)ints, st, a)))
+      return cuda_status(e);
   }
   ++g_launches;
   prof_mark(st, true);

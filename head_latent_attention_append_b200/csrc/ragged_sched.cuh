@@ -8,8 +8,8 @@
 // q_start[b + 1]; a row block walks the 64-key tiles that its last row sees.
 //
 // Every worker takes an equal, contiguous share of all tiles in row-block
-// order (a row block counts kBlockTiles more tiles for what it costs to change
-// query rows), so a share may cut a row block into pieces, which
+// order (a row block counts some more tiles for what it costs to change query
+// rows), so a share may cut a row block into pieces, which
 // ragged_combine_kernel merges.  All integer arithmetic: the cuts depend on
 // the lengths alone.
 #pragma once
@@ -89,6 +89,8 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   extern __shared__ int rs_smem[];
   int* const bs = rs_smem;  // [B+1] first row block of each request
   const int tid = threadIdx.x, nt = blockDim.x;
+  sm100::pdl_wait();
+  sm100::pdl_trigger();
   if (tid == 0) {
     *a.err = 0;
     *a.s.split_n = 0;
@@ -193,93 +195,107 @@ __device__ __forceinline__ float ref_max(float m) { return m == -INFINITY ? 0.f 
 __device__ __forceinline__ float row_inv(float l) { return l == 0.f ? 0.f : 1.f / l; }
 __device__ __forceinline__ float row_lse(float ref, float l) { return l == 0.f ? -INFINITY : ref + log2f(l); }
 
-// One CTA merges kCombineCols columns of a row block, its pieces in order.
-// Bound by latency (a few pieces of a few hundred KB in all, from L2), so a
-// thread asks for kBatch pieces at once (four rows, 16 bytes, of each).  The
-// rows' weights of a batch are made once per CTA, in shared memory.
-constexpr int kCombineCols = 32, kCombineThreads = 256, kBatch = 8;
+// One CTA merges kCombineCols columns of a row block, in order, kBatch pieces
+// at a time: their O (four rows, 16 bytes, per load) and (m, l) are asked for
+// together, then the rows' maximum, weights and sum are brought up to date in
+// shared memory as an online softmax does, and the batch is added.  Bound by
+// latency (some pieces of a few hundred KB in all, from L2), hence one pass.
+constexpr int kCombineCols = 16, kCombineThreads = 128, kBatch = 4;
 
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kCombineThreads) ragged_combine_kernel(RaggedSched S, RaggedOut o) {
   sm100::pdl_wait();
   sm100::pdl_trigger();
   constexpr int QUADS = ROWS / 4 * kCombineCols / kCombineThreads;  // (four rows, column) items per thread
-  __shared__ __align__(16) float coef[kBatch][ROWS];
-  __shared__ float top[ROWS], sum[ROWS];
+  constexpr int RPT = (ROWS + kCombineThreads - 1) / kCombineThreads;
+  static_assert(RPT == 1, "a thread keeps one row's state");
+  __shared__ __align__(16) float coef[kBatch + 1][ROWS];  // weights of the batch, factor for what came before
   __shared__ float tile[ROWS][kCombineCols + 1];
-  const int4 e = S.split[blockIdx.x];  // before the count is known: the entry exists
-  if ((int)blockIdx.x >= *S.split_n) return;
-  const int row0 = e.x, nrows = e.y, w0 = e.z, np = e.w, tid = threadIdx.x;
+  __shared__ float inv_of[ROWS];
+  const int tid = threadIdx.x, count = *S.split_n;
   const int col0 = blockIdx.y * kCombineCols, cols = min(kCombineCols, o.d_c - col0);
-  for (int r = tid; r < nrows; r += kCombineThreads) {
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int k = 0; k < np; ++k) m = fmaxf(m, __ldcg(&o.part_ml[(long long)ragged_slot(w0, k) * ROWS + r]).x);
-    top[r] = ref_max(m);
-    sum[r] = 0.f;
-  }
-  const int nq = (nrows + 3) / 4, items = nq * cols;  // consecutive items are consecutive in a slot's column
-  int off[QUADS], rq[QUADS];
-  float4 acc[QUADS];
-#pragma unroll
-  for (int i = 0; i < QUADS; ++i) {
-    const int x = tid + i * kCombineThreads, c = x / nq;
-    rq[i] = 4 * (x - c * nq);
-    off[i] = x < items ? (col0 + c) * ROWS + rq[i] : -1;
-    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  __syncthreads();
-  for (int k0 = 0; k0 < np; k0 += kBatch) {
-    const int kn = min(kBatch, np - k0);
-    for (int x = tid; x < kn * nrows; x += kCombineThreads) {
-      const int k = x / nrows, r = x - k * nrows;
-      const float2 ml = __ldcg(&o.part_ml[(long long)ragged_slot(w0, k0 + k) * ROWS + r]);
-      coef[k][r] = exp2f(ml.x - top[r]) * ml.y;
-    }
-    __syncthreads();
-    for (int r = tid; r < nrows; r += kCombineThreads) {
-      float l = sum[r];
-      for (int k = 0; k < kn; ++k) l += coef[k][r];
-      sum[r] = l;
-    }
+  for (int b = blockIdx.x; b < count; b += gridDim.x) {
+    const int4 e = S.split[b];
+    const int row0 = e.x, nrows = e.y, w0 = e.z, np = e.w;
+    const int nq = (nrows + 3) / 4, items = nq * cols;  // consecutive items are consecutive in a slot's column
+    int off[QUADS], rq[QUADS];
+    float4 acc[QUADS];
 #pragma unroll
     for (int i = 0; i < QUADS; ++i) {
-      if (off[i] < 0) continue;
-      float4 v[kBatch];
+      const int x = tid + i * kCombineThreads, c = x / nq;
+      rq[i] = 4 * (x - c * nq);
+      off[i] = x < items ? (col0 + c) * ROWS + rq[i] : -1;
+      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float m = -INFINITY, l = 0.f;  // of row `tid`
+    for (int k0 = 0; k0 < np; k0 += kBatch) {
+      float2 ml[kBatch];
+      float4 v[QUADS][kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (k < kn)
-          v[k] = __ldcg(reinterpret_cast<const float4*>(o.part_o + (long long)ragged_slot(w0, k0 + k) * o.d_c * ROWS + off[i]));
+      for (int k = 0; k < kBatch; ++k) {
+        const long long slot = ragged_slot(w0, k0 + k);
+        ml[k] = tid < nrows && k0 + k < np ? __ldcg(&o.part_ml[slot * ROWS + tid]) : make_float2(-INFINITY, 0.f);
+      }
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (k < kn) {
-          const float4 c = *reinterpret_cast<const float4*>(&coef[k][rq[i]]);
-          acc[i].x = fmaf(c.x, v[k].x, acc[i].x);
-          acc[i].y = fmaf(c.y, v[k].y, acc[i].y);
-          acc[i].z = fmaf(c.z, v[k].z, acc[i].z);
-          acc[i].w = fmaf(c.w, v[k].w, acc[i].w);
+      for (int i = 0; i < QUADS; ++i)
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const long long slot = ragged_slot(w0, k0 + k);
+          if (off[i] >= 0 && k0 + k < np) v[i][k] = __ldcg(reinterpret_cast<const float4*>(o.part_o + slot * o.d_c * ROWS + off[i]));
         }
+      if (tid < nrows) {
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
+        const float ref = ref_max(mn), f = exp2f(m - ref);
+        l *= f;
+        coef[kBatch][tid] = f;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const float w = exp2f(ml[k].x - ref) * ml[k].y;
+          coef[k][tid] = w;
+          l += w;
+        }
+        m = mn;
+        inv_of[tid] = row_inv(l);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < QUADS; ++i) {
+        if (off[i] < 0) continue;
+        const float4 f = *reinterpret_cast<const float4*>(&coef[kBatch][rq[i]]);
+        acc[i] = make_float4(acc[i].x * f.x, acc[i].y * f.y, acc[i].z * f.z, acc[i].w * f.w);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (k0 + k >= np) break;
+          const float4 c = *reinterpret_cast<const float4*>(&coef[k][rq[i]]);
+          acc[i].x = fmaf(c.x, v[i][k].x, acc[i].x);
+          acc[i].y = fmaf(c.y, v[i][k].y, acc[i].y);
+          acc[i].z = fmaf(c.z, v[i][k].z, acc[i].z);
+          acc[i].w = fmaf(c.w, v[i][k].w, acc[i].w);
+        }
+      }
+      __syncthreads();
+    }
+    // The rows behind nrows of a last group of four are never written to a
+    // slot; what they leave in the tile is not stored.
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i)
+      if (off[i] >= 0) {
+        const int c = off[i] / ROWS - col0;
+        tile[rq[i]][c] = acc[i].x;
+        tile[rq[i] + 1][c] = acc[i].y;
+        tile[rq[i] + 2][c] = acc[i].z;
+        tile[rq[i] + 3][c] = acc[i].w;
+      }
+    __syncthreads();
+    if (o.lse && blockIdx.y == 0 && tid < nrows) o.lse[(long long)row0 + tid] = row_lse(ref_max(m), l);
+    T* const dst = static_cast<T*>(o.out) + (long long)row0 * o.d_c + col0;
+    for (int x = tid; x < nrows * kCombineCols; x += kCombineThreads) {
+      const int r = x / kCombineCols, c = x % kCombineCols;
+      if (c < cols) dst[(long long)r * o.d_c + c] = from_f32<T>(tile[r][c] * inv_of[r]);
     }
     __syncthreads();
-  }
-  // The rows behind nrows of a last group of four are never written to a slot;
-  // what they leave in the tile is not stored.
-#pragma unroll
-  for (int i = 0; i < QUADS; ++i)
-    if (off[i] >= 0) {
-      const int c = off[i] / ROWS - col0;
-      tile[rq[i]][c] = acc[i].x;
-      tile[rq[i] + 1][c] = acc[i].y;
-      tile[rq[i] + 2][c] = acc[i].z;
-      tile[rq[i] + 3][c] = acc[i].w;
-    }
-  __syncthreads();
-  if (o.lse && blockIdx.y == 0)
-    for (int r = tid; r < nrows; r += kCombineThreads) o.lse[(long long)row0 + r] = row_lse(top[r], sum[r]);
-  T* const dst = static_cast<T*>(o.out) + (long long)row0 * o.d_c + col0;
-  for (int x = tid; x < nrows * kCombineCols; x += kCombineThreads) {
-    const int r = x / kCombineCols, c = x % kCombineCols;
-    if (c < cols) dst[(long long)r * o.d_c + c] = from_f32<T>(tile[r][c] * row_inv(sum[r]));
   }
 }
 
