@@ -90,11 +90,11 @@ struct PageWalk {
   RSeg g, gn;
   bool more;
   int page_next;
-  __device__ void start(int seg_lo) {
+  __device__ void start(int seg_lo, const RSeg& first) {
     si = seg_lo;
     more = si < seg_hi;
     if (!more) return;
-    g = segs[si];
+    g = first;
     gn = si + 1 < seg_hi ? segs[si + 1] : g;
     t = g.t_lo;
     page_next = page_table[(long long)g.seq * max_pages + t];
@@ -207,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int slot_bytes = score_ring ? SG_BYTES : VG_BYTES;
     const uint32_t full_even = map_peer(smem_u32(full), 0);
     PageWalk pw{segs, a.page_table, a.max_pages, 0, seg_hi, 0, RSeg{}, RSeg{}, false, 0};
-    pw.start(seg_lo);
+    pw.start(seg_lo, a.sched.first[w]);
     static_assert(VGS == 2, "two latent slots");
     uint32_t cnt = 0, part_cnt0 = 0, part_cnt1 = 0;  // edge loads per latent slot
     while (pw.more) {
@@ -438,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // its ends (three segments in registers were 4% slower, a ring of them in
     // shared memory 2%).
     if (seg_lo < seg_hi) {  // every softmax thread: q_store holds named barriers
-      q_issue(segs[seg_lo]);
+      q_issue(a.sched.first[w]);
       q_store();
     }
     for (int si = seg_lo; si < seg_hi; ++si) {

@@ -2,27 +2,46 @@
 // single-pass TF32 on the tensor cores would not keep.
 //
 // One CTA walks its worker's segments (ragged_sched.cuh) of up to 64 rows, 32
-// keys at a time: S = Q K^T in registers (thread (ty, tx): rows ty + 16 i,
-// keys tx + 16 j), the online softmax of a row among the 16 lanes that hold
-// it, and O += P V with 4 rows x 4 NG columns of O in each thread's registers.
-// A row's P is written and read by the same half-warp, so it costs no block
-// barrier.  Bound by the FMA pipe (a 16-byte shared-memory load feeds 4 to 16
-// FMAs); the loads of a key tile are about a tenth of its time, so there is
-// one buffer.  Row groups past the block's rows are skipped.
+// keys at a time; warp w keeps rows w, w + 8, ... of them, with their whole
+// softmax state, and works alone between the block's key tiles:
+//   S = Q K^T: lane (cg, kx) multiplies 8 rows with keys kx, kx + 8, kx + 16,
+//   kx + 24 over the columns 16 s + 4 cg ..; a reduce-scatter over the four
+//   column groups leaves lane `key` with the 8 rows' scores of that key;
+//   the online softmax of a row is then one warp reduction, and
+//   O += P V has 8 rows x 4 NC columns (4 lane + 128 c) in a lane's registers.
+// A 16-byte shared-memory load of a warp costs four cycles whatever it shares,
+// so a tile of R x C values per lane is bound by FMAs only where R C >= 4 (R +
+// C): 8 x 4 here (4 x 2 with 256 threads, or 2 x 2 with 512, were three and
+// four times above it and took 1.5 times as long), 8 x 4 NC in P V.  A small
+// batch is one tile per CTA and bound by latency, so all rows of a tile are
+// copied asynchronously at once, the next 32 keys while these are worked on
+// (where two buffers fit: rows of up to 432 values).
 #pragma once
 #include "ragged_sched.cuh"
 
 namespace mla {
 namespace ragged_simt {
 
-constexpr int ROWS = 64, KT = 32, THREADS = 256, PP = 36;
+constexpr int ROWS = 64, KT = 32, THREADS = 256, WARPS = THREADS / 32, PP = 36;
 
 // Columns are padded with zeros to whole float4s, the latent and the position
-// key separately; an odd number of float4s per row keeps the 16 rows of a
-// score load in different banks.
+// key separately, and the row to whole steps of 16; an odd number of float4s
+// per row keeps the 8 rows of a quarter warp's load in different banks.
 __host__ __device__ constexpr int pad4(int n) { return (n + 3) & ~3; }
-__host__ __device__ constexpr int pitch(int d_c, int d_r) { return 4 * (((pad4(d_c) + pad4(d_r)) / 4) | 1); }
-inline size_t smem_bytes(int d_c, int d_r) { return sizeof(float) * ((size_t)(ROWS + KT) * pitch(d_c, d_r) + ROWS * PP); }
+__host__ __device__ constexpr int row_cols(int d_c, int d_r) { return (pad4(d_c) + pad4(d_r) + 15) & ~15; }
+__host__ __device__ constexpr int pitch(int d_c, int d_r) { return row_cols(d_c, d_r) + 4; }
+inline size_t smem_bytes(int d_c, int d_r, int buffers) {
+  return sizeof(float) * ((size_t)(ROWS + buffers * KT) * pitch(d_c, d_r) + ROWS * PP);
+}
+constexpr size_t MAX_SMEM = 232448;
+inline int key_buffers(int d_c, int d_r) { return smem_bytes(d_c, d_r, 2) <= MAX_SMEM ? 2 : 1; }
+
+// 16 bytes from global to shared memory without passing through registers, or
+// zeros; both addresses 16-byte aligned.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool zero) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(zero ? 0 : 16)
+               : "memory");
+}
 
 struct Args {
   const float* q;            // row r of token t: q + t * q_ts + h * q_hs
@@ -30,165 +49,234 @@ struct Args {
   const float* cache;        // [num_pages][64][d_c + d_r]
   const int32_t* page_table; // [B][max_pages]
   int max_pages, num_pages, n_h, d_c, d_r;
+  int buffers;               // key tiles in shared memory, 1 or 2
   float scale;               // softmax scale times log2 e
   RaggedSched sched;
   RaggedOut o;
   int* err;
 };
 
-template <int NG>
-__global__ void __launch_bounds__(THREADS, 1) attn_ragged_simt_kernel(const Args a) {
+// Where a segment's rows and keys are.
+struct Ctx {
+  float *Qs, *Kb, *Ps;  // [ROWS][P4], [buffers][KT][P4], [ROWS][PP]
+  int d_cr, dcp, wq, P4;
+  bool vec;
+};
+
+// A small batch runs this kernel's code once, so what is not an inner loop is
+// kept small: the time of one tile was a third instruction misses while these
+// copies and stores were unrolled with both of their forms.
+//
+// One row into shared memory by a warp: the latent at 0, the position key at
+// dcp, zeros between and behind; not `live`: a row of zeros (src is then any
+// address in bounds).
+__device__ __noinline__ void put_row_any(float* dst, const float* src, bool live, int lane, int wq, int dcp, int d_c, int d_r) {
+  for (int c = lane; c < wq; c += 32) {
+    const int e = c < dcp ? (c < d_c ? c : -1) : (c - dcp < d_r ? d_c + c - dcp : -1);
+    dst[c] = live && e >= 0 ? __ldg(src + e) : 0.f;
+  }
+}
+__device__ __forceinline__ void put_row(const Args& a, const Ctx& x, float* dst, const float* src, bool live, int lane) {
+  if (x.vec) {
+#pragma unroll 1
+    for (int v = lane; v < x.wq / 4; v += 32) {
+      const bool in = 4 * v < x.d_cr;
+      copy16(dst + 4 * v, in ? src + 4 * v : src, !live || !in);
+    }
+  } else {
+    put_row_any(dst, src, live, lane, x.wq, x.dcp, a.d_c, a.d_r);
+  }
+}
+__device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float dot4(float4 q, float4 k, float s) {
+  return fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s))));
+}
+
+// A segment of at most 8 MI rows.  MI is a constant so that the loops over a
+// warp's rows leave no branches between loads and FMAs: with them the pipe was
+// a quarter used.
+template <int NC, int MI>
+__device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const RSeg& g) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kx = lane & 7, cg = lane >> 3, P4 = x.P4;
+  const int k_begin = g.t_lo * 64, k_end = min(g.nkeys, g.t_hi * 64);
+  const int32_t* const pages = a.page_table + (long long)g.seq * a.max_pages;
+  // The page of keys k0 .. is known one tile ahead of its copy.
+  int page_next = k_begin < k_end ? pages[k_begin / 64] : 0;
+  auto fetch = [&](int k0, float* dst) {
+    const int page = page_next;
+    const bool ok = page >= 0 && page < a.num_pages;
+    if (!ok && tid == 0) flag_error(a.err, kErrBounds);
+    const float* const src = a.cache + ((long long)(ok ? page : 0) * 64 + k0 % 64) * x.d_cr;
+#pragma unroll 1
+    for (int r = warp; r < KT; r += WARPS)
+      put_row(a, x, dst + r * P4, src + (long long)r * x.d_cr, ok && k0 + r < k_end, lane);
+    if (k0 + KT < k_end) page_next = pages[(k0 + KT) / 64];
+  };
+  __syncthreads();  // the segment before is done with Qs and the key tiles
+#pragma unroll 1
+  for (int i = 0; i < MI; ++i) {
+    const int r = warp + WARPS * i, row = g.row0 + min(r, g.nrows - 1), t = row / a.n_h;
+    put_row(a, x, x.Qs + r * P4, a.q + t * a.q_ts + (row - t * a.n_h) * a.q_hs, r < g.nrows, lane);
+  }
+  if (k_begin < k_end) fetch(k_begin, x.Kb);
+  int lim[MI];
+  float m[MI], l[MI], acc[MI][NC][4];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int r = warp + WARPS * i;
+    lim[i] = r < g.nrows ? min(max(g.base + (g.row0 + r) / a.n_h + 1, 0), g.nkeys) : 0;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.f;
+  }
+  float* const Pr = x.Ps + warp * PP;
+  int buf = 0;
+  for (int k0 = k_begin; k0 < k_end; k0 += KT, buf ^= a.buffers - 1) {
+    float* const Ks = x.Kb + buf * KT * P4;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();  // this tile is there, and every thread is done with the one before
+    if (a.buffers == 2 && k0 + KT < k_end) fetch(k0 + KT, x.Kb + (buf ^ 1) * KT * P4);
+    float s[MI][4];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    {
+      const float* const kp = Ks + kx * P4 + 4 * cg;
+      const float* const qp = x.Qs + warp * P4 + 4 * cg;
+      for (int c = 0; c < x.wq; c += 16) {
+        float4 k[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = at4(kp + 8 * j * P4 + c);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const float4 q = at4(qp + WARPS * i * P4 + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] = dot4(q, k[j], s[i][j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      // The four column groups' sums: this lane is left with key kx + 8 cg = lane.
+      const bool hi = cg & 2, odd = cg & 1;
+      const float t0 = (hi ? s[i][2] : s[i][0]) + __shfl_xor_sync(0xffffffffu, hi ? s[i][0] : s[i][2], 16);
+      const float t1 = (hi ? s[i][3] : s[i][1]) + __shfl_xor_sync(0xffffffffu, hi ? s[i][1] : s[i][3], 16);
+      const float sum4 = (odd ? t1 : t0) + __shfl_xor_sync(0xffffffffu, odd ? t0 : t1, 8);
+      const float sc = k0 + lane < lim[i] ? sum4 * a.scale : -INFINITY;
+      float mx = sc;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(m[i], mx), ref = ref_max(mn);
+      const float corr = exp2f(m[i] - ref), p = exp2f(sc - ref);
+      float sum = p;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l[i] = fmaf(l[i], corr, sum);
+      m[i] = mn;
+      Pr[WARPS * i * PP + lane] = p;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][c][e] *= corr;
+    }
+    __syncwarp();
+    if (k0 + KT > g.kmin) {
+      // Keys that only some of the rows see: a weight of 0 must not meet an
+      // infinity or a NaN.  A row that does see one already has a NaN sum.
+      __syncthreads();
+      for (int r = max(0, g.kmin - k0) + warp; r < KT; r += WARPS)
+        for (int c = lane; c < x.dcp; c += 32)
+          if (!isfinite(Ks[r * P4 + c])) Ks[r * P4 + c] = 0.f;
+      __syncthreads();
+    }
+    // A lane whose last columns lie behind the latent adds up what is there
+    // (the position key or zeros) and does not store it.
+#pragma unroll 1
+    for (int k = 0; k < KT; k += 4) {
+      float4 p[MI];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) p[i] = at4(Pr + WARPS * i * PP + k);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float4 v = at4(Ks + (k + kk) * P4 + min(4 * lane + 128 * c, x.wq - 4));
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+            acc[i][c][0] = fmaf(w, v.x, acc[i][c][0]);
+            acc[i][c][1] = fmaf(w, v.y, acc[i][c][1]);
+            acc[i][c][2] = fmaf(w, v.z, acc[i][c][2]);
+            acc[i][c][3] = fmaf(w, v.w, acc[i][c][3]);
+          }
+        }
+    }
+    __syncwarp();  // Ps is the next tile's
+    if (a.buffers == 1 && k0 + KT < k_end) {
+      __syncthreads();
+      fetch(k0 + KT, x.Kb);
+    }
+  }
+  // A whole row block goes to out, a piece to its slot (rows of dcp columns);
+  // where rows of `out` are not whole float4s, by way of this warp's own rows of
+  // Qs.
+  const bool wide = g.slot >= 0 || (a.d_c & 3) == 0;
+  float* const base = wide ? (g.slot < 0 ? static_cast<float*>(a.o.out) + (long long)g.row0 * x.dcp
+                                         : a.o.part_o + (long long)g.slot * ROWS * x.dcp)
+                           : x.Qs;
+  const int step = wide ? x.dcp : P4;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int r = warp + WARPS * i;
+    if (r >= g.nrows) continue;
+    const float inv = row_inv(l[i]);
+    float* const dst = base + r * step + 4 * lane;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (4 * lane + 128 * c < x.dcp)
+        *reinterpret_cast<float4*>(dst + 128 * c) =
+            make_float4(acc[i][c][0] * inv, acc[i][c][1] * inv, acc[i][c][2] * inv, acc[i][c][3] * inv);
+    if (lane == 0) {
+      if (g.slot >= 0) a.o.part_ml[(long long)g.slot * ROWS + r] = make_float2(m[i], l[i]);
+      else if (a.o.lse) a.o.lse[(long long)g.row0 + r] = row_lse(ref_max(m[i]), l[i]);
+    }
+  }
+  if (!wide) {
+    __syncwarp();
+#pragma unroll 1
+    for (int r = warp; r < g.nrows; r += WARPS)
+      for (int c = lane; c < a.d_c; c += 32)
+        static_cast<float*>(a.o.out)[((long long)g.row0 + r) * a.d_c + c] = x.Qs[r * P4 + c];
+  }
+}
+
+template <int NC>
+__global__ void __launch_bounds__(THREADS, 1) attn_ragged_simt_kernel(const __grid_constant__ Args a) {
   extern __shared__ float sm[];
-  const int d_cr = a.d_c + a.d_r, dcp = pad4(a.d_c), wq = dcp + pad4(a.d_r), P4 = pitch(a.d_c, a.d_r);
-  float* const Qs = sm;               // [ROWS][P4]
-  float* const Ks = Qs + ROWS * P4;   // [KT][P4]
-  float* const Ps = Ks + KT * P4;     // [ROWS][PP]
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
+  Ctx x;
+  x.d_cr = a.d_c + a.d_r;
+  x.dcp = pad4(a.d_c);
+  x.wq = row_cols(a.d_c, a.d_r);
+  x.P4 = pitch(a.d_c, a.d_r);
+  x.Qs = sm;
+  x.Kb = x.Qs + ROWS * x.P4;
+  x.Ps = x.Kb + a.buffers * KT * x.P4;
+  x.vec = (a.d_c & 3) == 0 && (x.d_cr & 3) == 0 && ((a.q_ts | a.q_hs) & 3) == 0 &&
+          ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.cache)) & 15) == 0;
   sm100::pdl_wait();
   sm100::pdl_trigger();
   const int seg_lo = a.sched.worker_seg[blockIdx.x], seg_hi = a.sched.worker_seg[blockIdx.x + 1];
-  const bool vec = (a.d_c & 3) == 0 && (d_cr & 3) == 0 && ((a.q_ts | a.q_hs) & 3) == 0 &&
-                   ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.cache)) & 15) == 0;
-  // One row into shared memory by a warp: the latent at 0, the position key
-  // at dcp, zeros between and behind; a null source is a row of zeros.
-  auto put_row = [&](float* dst, const float* src) {
-    if (vec) {
-      for (int v = lane; v < wq / 4; v += 32)
-        reinterpret_cast<float4*>(dst)[v] =
-            src && 4 * v < d_cr ? __ldg(reinterpret_cast<const float4*>(src) + v) : make_float4(0.f, 0.f, 0.f, 0.f);
-    } else {
-      for (int c = lane; c < wq; c += 32) {
-        const int e = c < dcp ? (c < a.d_c ? c : -1) : (c - dcp < a.d_r ? a.d_c + c - dcp : -1);
-        dst[c] = src && e >= 0 ? __ldg(src + e) : 0.f;
-      }
-    }
-  };
-
+  RSeg g = a.sched.first[blockIdx.x];
   for (int si = seg_lo; si < seg_hi; ++si) {
-    const RSeg g = a.sched.segs[si];
-    const int mi = ceil_div(g.nrows, 16);  // row groups that hold rows
-    __syncthreads();
-    for (int r = warp; r < 16 * mi; r += THREADS / 32) {
-      const int row = g.row0 + r, t = row / a.n_h;
-      put_row(Qs + r * P4, r < g.nrows ? a.q + t * a.q_ts + (row - t * a.n_h) * a.q_hs : nullptr);
-    }
-    int lim[4];
-    float m[4], l[4], acc[4][NG][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty + 16 * i;
-      lim[i] = r < g.nrows ? min(max(g.base + (g.row0 + r) / a.n_h + 1, 0), g.nkeys) : 0;
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-#pragma unroll
-      for (int c = 0; c < NG; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.f;
-    }
-    const int k_end = min(g.nkeys, g.t_hi * 64);
-    for (int k0 = g.t_lo * 64; k0 < k_end; k0 += KT) {
-      __syncthreads();
-      {
-        const int page = a.page_table[(long long)g.seq * a.max_pages + k0 / 64];
-        const bool ok = page >= 0 && page < a.num_pages;
-        if (!ok && tid == 0) flag_error(a.err, kErrBounds);
-        const float* const src = a.cache + ((long long)(ok ? page : 0) * 64 + k0 % 64) * d_cr;
-        for (int r = warp; r < KT; r += THREADS / 32)
-          put_row(Ks + r * P4, ok && k0 + r < k_end ? src + (long long)r * d_cr : nullptr);
-      }
-      __syncthreads();
-      float s[4][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = 0.f;
-      for (int c = 0; c < wq; c += 4) {
-        const float4 ka = *reinterpret_cast<const float4*>(Ks + tx * P4 + c);
-        const float4 kb = *reinterpret_cast<const float4*>(Ks + (tx + 16) * P4 + c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < mi) {
-            const float4 q = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * P4 + c);
-            s[i][0] = fmaf(q.x, ka.x, fmaf(q.y, ka.y, fmaf(q.z, ka.z, fmaf(q.w, ka.w, s[i][0]))));
-            s[i][1] = fmaf(q.x, kb.x, fmaf(q.y, kb.y, fmaf(q.z, kb.z, fmaf(q.w, kb.w, s[i][1]))));
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < mi) {
-          const float x0 = k0 + tx < lim[i] ? s[i][0] * a.scale : -INFINITY;
-          const float x1 = k0 + tx + 16 < lim[i] ? s[i][1] * a.scale : -INFINITY;
-          float mx = fmaxf(x0, x1);
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const float mn = fmaxf(m[i], mx), ref = ref_max(mn);
-          const float corr = exp2f(m[i] - ref), p0 = exp2f(x0 - ref), p1 = exp2f(x1 - ref);
-          float sum = p0 + p1;
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          l[i] = fmaf(l[i], corr, sum);
-          m[i] = mn;
-          Ps[(ty + 16 * i) * PP + tx] = p0;
-          Ps[(ty + 16 * i) * PP + tx + 16] = p1;
-#pragma unroll
-          for (int c = 0; c < NG; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][c][e] *= corr;
-        }
-      __syncwarp();
-      if (k0 + KT > g.kmin) {
-        // Keys that only some of the rows see: a weight of 0 must not meet an
-        // infinity or a NaN.  A row that does see one already has a NaN sum.
-        __syncthreads();
-        for (int x = tid; x < KT * dcp; x += THREADS) {
-          const int r = x / dcp, c = x - r * dcp;
-          if (k0 + r >= g.kmin && !isfinite(Ks[r * P4 + c])) Ks[r * P4 + c] = 0.f;
-        }
-        __syncthreads();
-      }
-#pragma unroll 2
-      for (int k = 0; k < KT; k += 4) {
-        float4 p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < mi) p[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * PP + k);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int c = 0; c < NG; ++c) {
-            if (4 * tx + 64 * c >= dcp) continue;
-            const float4 v = *reinterpret_cast<const float4*>(Ks + (k + kk) * P4 + 4 * tx + 64 * c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i < mi) {
-                const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-                acc[i][c][0] = fmaf(w, v.x, acc[i][c][0]);
-                acc[i][c][1] = fmaf(w, v.y, acc[i][c][1]);
-                acc[i][c][2] = fmaf(w, v.z, acc[i][c][2]);
-                acc[i][c][3] = fmaf(w, v.w, acc[i][c][3]);
-              }
-          }
-      }
-    }
-    // A whole row block goes to out, a piece to its slot (columns outermost).
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty + 16 * i;
-      if (r >= g.nrows) continue;
-      const float inv = row_inv(l[i]);
-      float* const dst = g.slot < 0 ? static_cast<float*>(a.o.out) + ((long long)g.row0 + r) * a.d_c
-                                    : a.o.part_o + (long long)g.slot * a.d_c * ROWS + r;
-      const int step = g.slot < 0 ? 1 : ROWS;
-#pragma unroll
-      for (int c = 0; c < NG; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = 4 * tx + 64 * c + e;
-          if (col < a.d_c) dst[(long long)col * step] = acc[i][c][e] * inv;
-        }
-      if (tx == 0) {
-        if (g.slot >= 0) a.o.part_ml[(long long)g.slot * ROWS + r] = make_float2(m[i], l[i]);
-        else if (a.o.lse) a.o.lse[(long long)g.row0 + r] = row_lse(ref_max(m[i]), l[i]);
-      }
-    }
+    if (si > seg_lo) g = a.sched.segs[si];
+    if (g.nrows <= 8) run_segment<NC, 1>(a, x, g);
+    else if (g.nrows <= 16) run_segment<NC, 2>(a, x, g);
+    else if (g.nrows <= 32) run_segment<NC, 4>(a, x, g);
+    else run_segment<NC, 8>(a, x, g);
   }
 }
 

@@ -13,7 +13,7 @@ constexpr int kRaggedPairs = 80, kRaggedCtas = 160;
 constexpr int kBlockTilesTc = 6, kBlockTilesSimt = 1;
 
 struct RaggedPlan {
-  size_t hdr, vs, pc, worker_seg, segs, split, part_o, part_ml, total;
+  size_t hdr, vs, pc, wf, worker_seg, segs, first, split, part_o, part_ml, total;
   int rows, cap, r_max;
 };
 RaggedPlan make_ragged_plan(const mla_dims& d, int B, int T) {
@@ -25,10 +25,12 @@ RaggedPlan make_ragged_plan(const mla_dims& d, int B, int T) {
   size_t o = 256;
   P.vs = o;         o = align_up(o + sizeof(int) * ((size_t)P.r_max + 1), 256);
   P.pc = o;         o = align_up(o + sizeof(int) * ((size_t)P.r_max + 1), 256);
+  P.wf = o;         o = align_up(o + sizeof(int) * ((size_t)P.r_max + 1), 256);
   P.worker_seg = o; o = align_up(o + sizeof(int) * ((size_t)P.cap + 1), 256);
   P.segs = o;       o = align_up(o + sizeof(RSeg) * ((size_t)P.cap + P.r_max), 256);
+  P.first = o;      o = align_up(o + sizeof(RSeg) * (size_t)P.cap, 256);
   P.split = o;      o = align_up(o + sizeof(int4) * (size_t)P.cap, 256);
-  P.part_o = o;     o = align_up(o + sizeof(float) * 2 * P.cap * P.rows * (size_t)d.d_c, 256);
+  P.part_o = o;     o = align_up(o + sizeof(float) * 2 * P.cap * P.rows * (size_t)align_up(d.d_c, 4), 256);
   P.part_ml = o;    o = align_up(o + sizeof(float2) * 2 * P.cap * P.rows, 256);
   P.total = o;
   return P;
@@ -67,11 +69,11 @@ cudaError_t launch_ragged_tc(const CUtensorMap& mapS, const CUtensorMap& mapV, c
   return launch_pdl(kfn, dim3(2 * W), dim3(ragged_tc::THREADS), ragged_tc::SMEM_BYTES, st, mapS, mapV, a);
 }
 
-template <int NG>
+template <int NC>
 cudaError_t launch_ragged_simt(const ragged_simt::Args& a, int W, cudaStream_t st) {
-  auto kfn = ragged_simt::attn_ragged_simt_kernel<NG>;
-  const size_t sm = ragged_simt::smem_bytes(a.d_c, a.d_r);
-  cudaError_t e = set_smem_once(kfn, ragged_simt::smem_bytes(512, 64));  // the largest of every width
+  auto kfn = ragged_simt::attn_ragged_simt_kernel<NC>;
+  const size_t sm = ragged_simt::smem_bytes(a.d_c, a.d_r, a.buffers);
+  cudaError_t e = set_smem_once(kfn, ragged_simt::MAX_SMEM);
   if (e) return e;
   return launch_pdl(kfn, dim3(W), dim3(ragged_simt::THREADS), sm, st, a);
 }
@@ -120,13 +122,13 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
   const int W = std::max(1, std::min(P.cap, tc ? num_sms() / 2 : num_sms()));
   const float scale =
       (float)((d.softmax_scale > 0.f ? (double)d.softmax_scale : 1.0 / sqrt((double)(d.d_h + d.d_r))) * kLog2e);
-  const RaggedSched S{at<int>(ws, P.vs), at<int>(ws, P.pc), at<int>(ws, P.worker_seg), at<RSeg>(ws, P.segs),
-                      at<int>(ws, P.hdr) + 1, at<int4>(ws, P.split)};
+  const RaggedSched S{at<int>(ws, P.vs), at<int>(ws, P.pc), at<int>(ws, P.wf), at<int>(ws, P.worker_seg),
+                      at<RSeg>(ws, P.segs), at<RSeg>(ws, P.first), at<int>(ws, P.hdr) + 1, at<int4>(ws, P.split)};
   const RaggedOut o{out, lse, at<float>(ws, P.part_o), at<float2>(ws, P.part_ml), d.d_c};
   int* err = at<int>(ws, P.hdr);
   cudaError_t e;
   {
-    const int ints = (int)std::min<long long>(B + 1 + 2LL * (P.r_max + 1), kRaggedSmemInts);
+    const int ints = (int)std::min<long long>(B + 1 + 3LL * (P.r_max + 1), kRaggedSmemInts);
     const RaggedSchedArgs a{q_start, kv_len, B, T, d.n_h, P.rows, W, max_pages, P.r_max,
                             tc ? kBlockTilesTc : kBlockTilesSimt, S, err, ints};
     if ((e = set_smem_once(ragged_sched_kernel, sizeof(int) * (size_t)kRaggedSmemInts))) return cuda_status(e);
@@ -152,18 +154,17 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
     }
   } else {
     ragged_simt::Args a{static_cast<const float*>(q), q_ts, q_hs, static_cast<const float*>(cache), page_table,
-                        max_pages, num_pages, d.n_h, d.d_c, d.d_r, scale, S, o, err};
-    if (d.d_c <= 64) e = launch_ragged_simt<1>(a, W, st);
-    else if (d.d_c <= 128) e = launch_ragged_simt<2>(a, W, st);
-    else if (d.d_c <= 256) e = launch_ragged_simt<4>(a, W, st);
-    else e = launch_ragged_simt<8>(a, W, st);
+                        max_pages, num_pages, d.n_h, d.d_c, d.d_r, ragged_simt::key_buffers(d.d_c, d.d_r), scale, S, o, err};
+    if (d.d_c <= 128) e = launch_ragged_simt<1>(a, W, st);
+    else if (d.d_c <= 256) e = launch_ragged_simt<2>(a, W, st);
+    else e = launch_ragged_simt<4>(a, W, st);
   }
   if (e) return cuda_status(e);
   prof_mark(st, false);
   ++g_launches;
   const dim3 grid(W, ceil_div(d.d_c, kCombineCols));
-  if (tc) e = launch_pdl(ragged_combine_kernel<__nv_bfloat16, ragged_tc::ROWS>, grid, dim3(kCombineThreads), 0, st, S, o);
-  else e = launch_pdl(ragged_combine_kernel<float, ragged_simt::ROWS>, grid, dim3(kCombineThreads), 0, st, S, o);
+  if (tc) e = launch_pdl(ragged_combine_kernel<__nv_bfloat16, ragged_tc::ROWS, true>, grid, dim3(kCombineThreads), 0, st, S, o);
+  else e = launch_pdl(ragged_combine_kernel<float, ragged_simt::ROWS, false>, grid, dim3(kCombineThreads), 0, st, S, o);
   return cuda_status(e);
 }
 

@@ -35,8 +35,10 @@ struct __align__(16) RSeg {
 struct RaggedSched {
   int* vs;          // [R+1] first (weighted) tile of each row block
   int* pc;          // [R+1] first segment of each row block
+  int* wf;          // [R]   worker of that segment
   int* worker_seg;  // [W+1] first segment of each worker
   RSeg* segs;       // [W+R]
+  RSeg* first;      // [W]   a copy of each worker's first segment, which it reads beside its two numbers
   int* split_n;     // row blocks in pieces, and
   int4* split;      // [W] for each: first row, rows, worker of the first piece, pieces (one per worker from there on)
 };
@@ -55,8 +57,10 @@ struct RaggedSchedArgs {
 };
 
 // Exclusive scan in place, with the total in 64 bits (data[] is meaningless
-// if that does not fit in 32).
-__device__ long long ragged_scan(int* data, int n) {
+// if that does not fit in 32).  Out of line: the schedule is one pass over cold
+// code, and a third of its time was instruction misses while this was in it
+// three times.
+__device__ __noinline__ long long ragged_scan(int* data, int n) {
   __shared__ long long wide[32];
   const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int chunk = (n + T - 1) / T, lo = min(n, tid * chunk), hi = min(n, lo + chunk);
@@ -113,9 +117,10 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   }
   const int R = (int)ragged_scan(bs, a.B);  // <= r_max: the starts are in order
   if (tid == 0) bs[a.B] = R;
-  const bool in_smem = a.B + 1 + 2 * (R + 1) <= a.smem_ints;
+  const bool in_smem = a.B + 1 + 3 * (R + 1) <= a.smem_ints;
   int* const vs = in_smem ? bs + a.B + 1 : a.s.vs;
   int* const pc = in_smem ? vs + R + 1 : a.s.pc;
+  int* const wf = in_smem ? pc + R + 1 : a.s.wf;
   __syncthreads();
 
   auto block = [&](int rb) {
@@ -142,32 +147,35 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   const int total = (int)total64;
   if (tid == 0) vs[R] = total;
   const int W = min(a.W, total);  // every worker's share has at least one tile
-  // The worker whose share [w total / W, (w + 1) total / W) holds tile x.
-  const bool narrow = (long long)total * W < 0x7fffffffLL;  // 64-bit divisions cost a microsecond here
-  auto owner = [&](int x) {
-    return narrow ? (int)(((unsigned)(x + 1) * (unsigned)W - 1u) / (unsigned)total)
-                  : (int)((((long long)x + 1) * W - 1) / total);
-  };
-  auto share = [&](int w) {  // first tile of worker w's share
-    return narrow ? (int)((unsigned)w * (unsigned)total / (unsigned)W) : (int)((long long)w * total / W);
+  // Worker w's share starts at tile w len + min(w, rest).
+  const int len = total / W, rest = total - len * W, longer = rest * (len + 1);
+  auto share = [&](int w) { return w * len + min(w, rest); };
+  auto owner = [&](int x) {  // the worker whose share holds tile x
+    const bool in = x < longer;
+    return (in ? 0 : rest) + (x - (in ? 0 : longer)) / (in ? len + 1 : len);
   };
   __syncthreads();
-  for (int rb = tid; rb < R; rb += nt) pc[rb] = owner(vs[rb + 1] - 1) - owner(vs[rb] + a.block_tiles) + 1;
+  for (int rb = tid; rb < R; rb += nt) {
+    wf[rb] = owner(vs[rb] + a.block_tiles);
+    pc[rb] = owner(vs[rb + 1] - 1) - wf[rb] + 1;
+  }
   __syncthreads();
   const int nseg = (int)ragged_scan(pc, R);  // <= R + W
   if (tid == 0) pc[R] = nseg;
   __syncthreads();
   for (int s = tid; s < nseg; s += nt) {
     const int rb = find_le(pc, R, s), k = s - pc[rb], pieces = pc[rb + 1] - pc[rb];
-    const int first = vs[rb] + a.block_tiles, w = owner(first) + k;
+    const int start = vs[rb] + a.block_tiles, w = wf[rb] + k;
     RSeg g = block(rb);
-    g.t_lo = max(share(w) - first, 0);
-    g.t_hi = min(share(w + 1), vs[rb + 1]) - first;
+    g.t_lo = max(share(w) - start, 0);
+    g.t_hi = min(share(w + 1), vs[rb + 1]) - start;
     // Only the first and the last segment of a worker can be pieces.
     g.slot = pieces == 1 ? -1 : ragged_slot(w - k, k);
     g.pad[0] = g.pad[1] = g.pad[2] = 0;
     a.s.segs[s] = g;
-    const int before = k > 0 ? w - 1 : (rb > 0 ? owner(vs[rb] - 1) : -1);  // the previous segment's worker
+    // The previous segment's worker; the ones behind it, up to this one, start here.
+    const int before = k > 0 ? w - 1 : (rb > 0 ? wf[rb - 1] + s - pc[rb - 1] - 1 : -1);
+    if (before < w) a.s.first[w] = g;
     for (int v = before + 1; v <= w; ++v) a.s.worker_seg[v] = s;
     if (s == nseg - 1)
       for (int v = w + 1; v <= a.W; ++v) a.s.worker_seg[v] = nseg;
@@ -176,14 +184,16 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
 }
 
 // ------------------------------------------------------------------ combine
-// What the attention kernels leave of a row block in pieces: in slot s, column
-// by column, the piece's O / l (32 bits, rows contiguous, so that both sides
-// move whole lines), and its (m, l) per row, in base 2:
+// What the attention kernels leave of a row block in pieces: per slot s the
+// piece's O / l in 32 bits and its (m, l) per row, in base 2:
 //   m = max m_s,  l = sum 2^(m_s - m) l_s,  o = sum 2^(m_s - m) l_s N_s / l.
+// The tensor-core kernel writes a slot column by column (rows contiguous, as
+// its threads hold them), the CUDA-core kernel row by row (d_c padded to whole
+// float4s), so that both move whole lines.
 struct RaggedOut {
   void* out;       // [T * n_h][d_c]
   float* lse;      // [T * n_h] or null
-  float* part_o;   // [2W][d_c][ROWS]
+  float* part_o;   // [2W][d_c][ROWS], or [2W][ROWS][d_c padded]
   float2* part_ml; // [2W][ROWS]
   int d_c;
 };
@@ -196,106 +206,127 @@ __device__ __forceinline__ float row_inv(float l) { return l == 0.f ? 0.f : 1.f 
 __device__ __forceinline__ float row_lse(float ref, float l) { return l == 0.f ? -INFINITY : ref + log2f(l); }
 
 // One CTA merges kCombineCols columns of a row block, in order, kBatch pieces
-// at a time: their O (four rows, 16 bytes, per load) and (m, l) are asked for
-// together, then the rows' maximum, weights and sum are brought up to date in
-// shared memory as an online softmax does, and the batch is added.  Bound by
-// latency (some pieces of a few hundred KB in all, from L2), hence one pass.
+// at a time: their O (16 bytes per load: four rows of a column, or four columns
+// of a row) and (m, l) are asked for together, then the rows' maximum, weights
+// and sum are brought up to date in shared memory as an online softmax does,
+// and the batch is added.  Bound by latency (some pieces of a few hundred KB
+// in all, from L2), hence one pass.
 constexpr int kCombineCols = 16, kCombineThreads = 128, kBatch = 4;
 
-template <typename T, int ROWS>
+template <typename T, int ROWS, bool kByColumn>
 __global__ void __launch_bounds__(kCombineThreads) ragged_combine_kernel(RaggedSched S, RaggedOut o) {
   sm100::pdl_wait();
   sm100::pdl_trigger();
-  constexpr int QUADS = ROWS / 4 * kCombineCols / kCombineThreads;  // (four rows, column) items per thread
-  constexpr int RPT = (ROWS + kCombineThreads - 1) / kCombineThreads;
-  static_assert(RPT == 1, "a thread keeps one row's state");
+  constexpr int QUADS = ROWS * kCombineCols / 4 / kCombineThreads;  // 16-byte items per thread
+  static_assert(ROWS <= kCombineThreads && QUADS >= 1, "a thread keeps one row's state");
   __shared__ __align__(16) float coef[kBatch + 1][ROWS];  // weights of the batch, factor for what came before
-  __shared__ float tile[ROWS][kCombineCols + 1];
+  __shared__ float tile[kByColumn ? ROWS : 1][kCombineCols + 1];
   __shared__ float inv_of[ROWS];
-  const int tid = threadIdx.x, count = *S.split_n;
+  const int tid = threadIdx.x;
+  const int4 e = S.split[blockIdx.x];  // asked for before the count is known
+  if ((int)blockIdx.x >= *S.split_n) return;
+  const int row0 = e.x, nrows = e.y, w0 = e.z, np = e.w;
   const int col0 = blockIdx.y * kCombineCols, cols = min(kCombineCols, o.d_c - col0);
-  for (int b = blockIdx.x; b < count; b += gridDim.x) {
-    const int4 e = S.split[b];
-    const int row0 = e.x, nrows = e.y, w0 = e.z, np = e.w;
-    const int nq = (nrows + 3) / 4, items = nq * cols;  // consecutive items are consecutive in a slot's column
-    int off[QUADS], rq[QUADS];
-    float4 acc[QUADS];
+  const int pitch = kByColumn ? o.d_c : (o.d_c + 3) & ~3;
+  const long long slot_elems = (long long)pitch * ROWS;
+  // Items: quads of rows of a column (consecutive in the slot's column), or
+  // quads of columns of a row.  pos: the row (of the first of the four), lane
+  // of the item within it: the column.
+  const int minor = kByColumn ? (nrows + 3) / 4 : (cols + 3) / 4;
+  const int items = minor * (kByColumn ? cols : nrows);
+  int row[QUADS], col[QUADS];
+  float4 acc[QUADS];
 #pragma unroll
-    for (int i = 0; i < QUADS; ++i) {
-      const int x = tid + i * kCombineThreads, c = x / nq;
-      rq[i] = 4 * (x - c * nq);
-      off[i] = x < items ? (col0 + c) * ROWS + rq[i] : -1;
-      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < QUADS; ++i) {
+    const int x = tid + i * kCombineThreads, major = x / minor, quad = 4 * (x - major * minor);
+    row[i] = x < items ? (kByColumn ? quad : major) : -1;
+    col[i] = col0 + (kByColumn ? major : quad);
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float m = -INFINITY, l = 0.f;  // of row `tid`
+  for (int k0 = 0; k0 < np; k0 += kBatch) {
+    float2 ml[kBatch];
+    float4 v[QUADS][kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const long long slot = ragged_slot(w0, k0 + k);
+      ml[k] = tid < nrows && k0 + k < np ? __ldcg(&o.part_ml[slot * ROWS + tid]) : make_float2(-INFINITY, 0.f);
     }
-    float m = -INFINITY, l = 0.f;  // of row `tid`
-    for (int k0 = 0; k0 < np; k0 += kBatch) {
-      float2 ml[kBatch];
-      float4 v[QUADS][kBatch];
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i)
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (row[i] >= 0 && k0 + k < np) {
+          const long long off = kByColumn ? (long long)col[i] * ROWS + row[i] : (long long)row[i] * pitch + col[i];
+          v[i][k] = __ldcg(reinterpret_cast<const float4*>(o.part_o + ragged_slot(w0, k0 + k) * slot_elems + off));
+        }
+    if (tid < nrows) {
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
+      const float ref = ref_max(mn), f = exp2f(m - ref);
+      l *= f;
+      coef[kBatch][tid] = f;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const long long slot = ragged_slot(w0, k0 + k);
-        ml[k] = tid < nrows && k0 + k < np ? __ldcg(&o.part_ml[slot * ROWS + tid]) : make_float2(-INFINITY, 0.f);
+        const float w = exp2f(ml[k].x - ref) * ml[k].y;
+        coef[k][tid] = w;
+        l += w;
       }
-#pragma unroll
-      for (int i = 0; i < QUADS; ++i)
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const long long slot = ragged_slot(w0, k0 + k);
-          if (off[i] >= 0 && k0 + k < np) v[i][k] = __ldcg(reinterpret_cast<const float4*>(o.part_o + slot * o.d_c * ROWS + off[i]));
-        }
-      if (tid < nrows) {
-        float mn = m;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
-        const float ref = ref_max(mn), f = exp2f(m - ref);
-        l *= f;
-        coef[kBatch][tid] = f;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const float w = exp2f(ml[k].x - ref) * ml[k].y;
-          coef[k][tid] = w;
-          l += w;
-        }
-        m = mn;
-        inv_of[tid] = row_inv(l);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < QUADS; ++i) {
-        if (off[i] < 0) continue;
-        const float4 f = *reinterpret_cast<const float4*>(&coef[kBatch][rq[i]]);
-        acc[i] = make_float4(acc[i].x * f.x, acc[i].y * f.y, acc[i].z * f.z, acc[i].w * f.w);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          if (k0 + k >= np) break;
-          const float4 c = *reinterpret_cast<const float4*>(&coef[k][rq[i]]);
-          acc[i].x = fmaf(c.x, v[i][k].x, acc[i].x);
-          acc[i].y = fmaf(c.y, v[i][k].y, acc[i].y);
-          acc[i].z = fmaf(c.z, v[i][k].z, acc[i].z);
-          acc[i].w = fmaf(c.w, v[i][k].w, acc[i].w);
-        }
-      }
-      __syncthreads();
+      m = mn;
+      inv_of[tid] = row_inv(l);
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i) {
+      if (row[i] < 0) continue;
+      auto weights = [&](int k) {
+        if constexpr (kByColumn) return *reinterpret_cast<const float4*>(&coef[k][row[i]]);
+        const float c = coef[k][row[i]];
+        return make_float4(c, c, c, c);
+      };
+      const float4 f = weights(kBatch);
+      acc[i] = make_float4(acc[i].x * f.x, acc[i].y * f.y, acc[i].z * f.z, acc[i].w * f.w);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (k0 + k >= np) break;
+        const float4 c = weights(k);
+        acc[i].x = fmaf(c.x, v[i][k].x, acc[i].x);
+        acc[i].y = fmaf(c.y, v[i][k].y, acc[i].y);
+        acc[i].z = fmaf(c.z, v[i][k].z, acc[i].z);
+        acc[i].w = fmaf(c.w, v[i][k].w, acc[i].w);
+      }
+    }
+    __syncthreads();
+  }
+  if (o.lse && blockIdx.y == 0 && tid < nrows) o.lse[(long long)row0 + tid] = row_lse(ref_max(m), l);
+  T* const dst = static_cast<T*>(o.out) + (long long)row0 * o.d_c;
+  if constexpr (kByColumn) {
     // The rows behind nrows of a last group of four are never written to a
     // slot; what they leave in the tile is not stored.
 #pragma unroll
     for (int i = 0; i < QUADS; ++i)
-      if (off[i] >= 0) {
-        const int c = off[i] / ROWS - col0;
-        tile[rq[i]][c] = acc[i].x;
-        tile[rq[i] + 1][c] = acc[i].y;
-        tile[rq[i] + 2][c] = acc[i].z;
-        tile[rq[i] + 3][c] = acc[i].w;
+      if (row[i] >= 0) {
+        const int c = col[i] - col0;
+        tile[row[i]][c] = acc[i].x;
+        tile[row[i] + 1][c] = acc[i].y;
+        tile[row[i] + 2][c] = acc[i].z;
+        tile[row[i] + 3][c] = acc[i].w;
       }
     __syncthreads();
-    if (o.lse && blockIdx.y == 0 && tid < nrows) o.lse[(long long)row0 + tid] = row_lse(ref_max(m), l);
-    T* const dst = static_cast<T*>(o.out) + (long long)row0 * o.d_c + col0;
     for (int x = tid; x < nrows * kCombineCols; x += kCombineThreads) {
       const int r = x / kCombineCols, c = x % kCombineCols;
-      if (c < cols) dst[(long long)r * o.d_c + c] = from_f32<T>(tile[r][c] * inv_of[r]);
+      if (c < cols) dst[(long long)r * o.d_c + col0 + c] = from_f32<T>(tile[r][c] * inv_of[r]);
     }
-    __syncthreads();
+  } else {
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i)
+      if (row[i] >= 0) {
+        const float f = inv_of[row[i]], w[4] = {acc[i].x, acc[i].y, acc[i].z, acc[i].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (col[i] + c < o.d_c) dst[(long long)row[i] * o.d_c + col[i] + c] = from_f32<T>(w[c] * f);
+      }
   }
 }
 
