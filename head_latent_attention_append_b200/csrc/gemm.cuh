@@ -66,6 +66,7 @@ struct EpiAppend {
   OutT* dense;             // optional: every row also at dense[m * d_cr] (token order), else null
   const int32_t* kv_len;   // decode step: lengths after the append, and
   int n_q;                 // new tokens per sequence
+  int padded;              // seq_idx -1 marks a row of no sequence, which is left out
   __device__ void locate(int m, int& s, int& p) const {
     if (seq_idx) {
       s = seq_idx[m];
@@ -81,6 +82,7 @@ struct EpiAppend {
   __device__ void operator()(int, int m, int n, float v0, float v1) const {
     int s, p;
     locate(m, s, p);
+    if (padded && s == -1) return;
     if (s < 0 || s >= n_seq || p < 0 || p >= max_pages * page_size) {
       flag_error(err, kErrBounds);
       return;
@@ -99,6 +101,7 @@ struct EpiAppend {
   __device__ void store8(int, int m, int n0, const float (&v)[8]) const {
     int s, p;
     locate(m, s, p);
+    if (padded && s == -1) return;
     if (s < 0 || s >= n_seq || p < 0 || p >= max_pages * page_size) {
       flag_error(err, kErrBounds);
       return;
@@ -132,6 +135,12 @@ struct EpiQProj {
   double theta[32];
   int n_h, d_h, d_r, d_c, d_cr, qabs_rows, n_q, prefill_S;
   float qr_scale;
+  const int32_t* pos;      // ragged step: the token's position, else null
+  __device__ int position(int m) const {
+    if (pos) return pos[m];
+    if (prefill_S > 0) return m % prefill_S;
+    return (kv_len ? kv_len[m / n_q] : uniform_kv_len) - n_q + m % n_q;
+  }
   __device__ void operator()(int, int m, int n, float v0, float v1) const {
     const int nc = n_h * d_h;
     if (n < nc) {
@@ -139,10 +148,7 @@ struct EpiQProj {
       return;
     }
     int j = n - nc, h = j / d_r, jj = j - h * d_r;
-    int p;
-    if (prefill_S > 0) p = m % prefill_S;
-    else p = (kv_len ? kv_len[m / n_q] : uniform_kv_len) - n_q + m % n_q;
-    rope_rotate_pair(v0, v1, p, theta[jj >> 1]);
+    rope_rotate_pair(v0, v1, position(m), theta[jj >> 1]);
     store_pair(qabs + ((long long)m * qabs_rows + h) * d_cr + d_c + jj, qr_scale * v0, qr_scale * v1);
   }
   // Columns n0 .. n0 + 7 of token m (n0 a multiple of 8; n_h*d_h and d_r are
@@ -154,9 +160,7 @@ struct EpiQProj {
       return;
     }
     const int j = n0 - nc, h = j / d_r, jj = j - h * d_r;
-    int p;
-    if (prefill_S > 0) p = m % prefill_S;
-    else p = (kv_len ? kv_len[m / n_q] : uniform_kv_len) - n_q + m % n_q;
+    const int p = position(m);
     float w[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

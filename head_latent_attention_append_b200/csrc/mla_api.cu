@@ -492,9 +492,10 @@ mla_status append_impl(const mla_weights* w, const void* h, const int32_t* seq_i
                        int prefill_S, int n_seq, const int32_t* page_table, int max_pages, int num_pages,
                        void* cache, int T_, void* ws, const Plan& P, cudaStream_t st,
                        const int32_t* kv_len = nullptr, int n_q = 0, int tile_split_cap = kSplitKTileSplits,
-                       int max_ctas = INT_MAX) {
+                       int max_ctas = INT_MAX, bool padded = false) {
   const mla_dims& d = w->d;
   EpiAppend<T> epi{};
+  epi.padded = padded;
   epi.cache = static_cast<T*>(cache);
   epi.seq_idx = seq_idx;
   epi.pos = pos;

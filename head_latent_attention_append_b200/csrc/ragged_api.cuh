@@ -113,11 +113,13 @@ void launch_query(step::QueryArgs& a, bool vec, cudaStream_t st) {
   else launch_query<T, true, 32, 4>(a, st);
 }
 
-// Schedule, attention, merge of the row blocks in pieces.
+// Schedule, attention, merge of the row blocks in pieces.  `err`: the error
+// word, zeroed by the schedule unless an earlier launch of the call reports
+// there too.
 mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, long long q_hs, const int32_t* q_start,
                               const int32_t* kv_len, const int32_t* page_table, int B, int T, int max_pages,
                               int num_pages, const void* cache, void* out, float* lse, void* ws, const RaggedPlan& P,
-                              cudaStream_t st) {
+                              int* err, bool keep_err, cudaStream_t st) {
   const bool tc = d.dtype == MLA_BF16;
   const int W = std::max(1, std::min(P.cap, tc ? num_sms() / 2 : num_sms()));
   const float scale =
@@ -125,12 +127,11 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
   const RaggedSched S{at<int>(ws, P.vs), at<int>(ws, P.pc), at<int>(ws, P.wf), at<int>(ws, P.worker_seg),
                       at<RSeg>(ws, P.segs), at<RSeg>(ws, P.first), at<int>(ws, P.hdr) + 1, at<int4>(ws, P.split)};
   const RaggedOut o{out, lse, at<float>(ws, P.part_o), at<float2>(ws, P.part_ml), d.d_c};
-  int* err = at<int>(ws, P.hdr);
   cudaError_t e;
   {
     const int ints = (int)std::min<long long>(B + 1 + 3LL * (P.r_max + 1), kRaggedSmemInts);
     const RaggedSchedArgs a{q_start, kv_len, B, T, d.n_h, P.rows, W, max_pages, P.r_max,
-                            tc ? kBlockTilesTc : kBlockTilesSimt, S, err, ints};
+                            tc ? kBlockTilesTc : kBlockTilesSimt, keep_err, S, err, ints};
     if ((e = set_smem_once(ragged_sched_kernel, sizeof(int) * (size_t)kRaggedSmemInts))) return cuda_status(e);
     ++g_launches;
     if ((e = launch_pdl(ragged_sched_kernel, dim3(1), dim3(P.r_max > 1024 ? 1024 : 256), sizeof(int) * (size_t)ints, st, a)))
@@ -166,6 +167,78 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
   if (tc) e = launch_pdl(ragged_combine_kernel<__nv_bfloat16, ragged_tc::ROWS, true>, grid, dim3(kCombineThreads), 0, st, S, o);
   else e = launch_pdl(ragged_combine_kernel<float, ragged_simt::ROWS, false>, grid, dim3(kCombineThreads), 0, st, S, o);
   return cuda_status(e);
+}
+
+// The whole ragged step from hidden states: the projections' scratch first
+// (its header holds the error word), then the intermediates, then the ragged
+// attention's workspace.
+struct RaggedStepPlan {
+  Plan base;  // hdr, counters, partial
+  size_t cq, qc, qabs, obar, ragged, total;
+  RaggedPlan attend;
+};
+RaggedStepPlan make_ragged_step_plan(const mla_dims& d, int B, int T) {
+  RaggedStepPlan P{};
+  const size_t e = esize(d), n = (size_t)T * d.n_h;
+  P.base = make_plan(d, T, false);
+  size_t o = P.base.total;
+  P.cq = o;     o = align_up(o + e * (size_t)T * d.d_cq, 256);
+  P.qc = o;     o = align_up(o + e * n * d.d_h, 256);
+  P.qabs = o;   o = align_up(o + e * n * (d.d_c + d.d_r), 256);
+  P.obar = o;   o = align_up(o + e * n * d.d_c, 256);
+  P.ragged = o;
+  P.attend = make_ragged_plan(d, B, T);
+  P.total = o + P.attend.total;
+  return P;
+}
+
+template <typename T>
+mla_status ragged_step_impl(const mla_weights* w, const void* h, const int32_t* q_start, const int32_t* kv_len,
+                            const int32_t* seq_idx, const int32_t* pos, const int32_t* page_table, int B, int T_,
+                            int max_pages, int num_pages, void* cache, float* out, void* ws, const RaggedStepPlan& P,
+                            cudaStream_t st) {
+  const mla_dims& d = w->d;
+  const int din = d_in(d), q_row = d.d_c + d.d_r;
+  cudaError_t e;
+  // (1) the new tokens' cache rows.
+  mla_status s = append_impl<T>(w, h, seq_idx, pos, 0, B, page_table, max_pages, num_pages, cache, T_, ws, P.base, st,
+                                nullptr, 0, kSplitKTileSplits, INT_MAX, true);
+  if (s != MLA_OK) return s;
+  // (2) query latent, (3) q_C and the rotated q_R, (4) absorption.  The scale
+  // is the attention's, in 32 bits.
+  const void* src = h;
+  if (d.d_cq > 0) {
+    EpiStore<T> epi{at<T>(ws, P.cq), d.d_cq, 0, 1.f};
+    if ((e = gemm<T>(h, d.d_model, 0, w->dq, d.d_model, 0, T_, d.d_cq, d.d_model, 1, epi, ws, P.base, st)))
+      return cuda_status(e);
+    src = at<T>(ws, P.cq);
+  }
+  {
+    EpiQProj<T> epi{};
+    epi.qc = at<T>(ws, P.qc);
+    epi.qabs = at<T>(ws, P.qabs);
+    for (int i = 0; i < d.d_r / 2; ++i) epi.theta[i] = w->theta[i];
+    epi.n_h = d.n_h; epi.d_h = d.d_h; epi.d_r = d.d_r; epi.d_c = d.d_c; epi.d_cr = q_row;
+    epi.qabs_rows = d.n_h;
+    epi.qr_scale = 1.f;
+    epi.pos = pos;
+    if ((e = gemm<T>(src, din, 0, w->uqr, din, 0, T_, d.n_h * (d.d_h + d.d_r), din, 1, epi, ws, P.base, st)))
+      return cuda_status(e);
+  }
+  {
+    EpiStore<T> epi{at<T>(ws, P.qabs), (long long)d.n_h * q_row, q_row, 1.f};
+    if ((e = gemm<T>(at<T>(ws, P.qc), (long long)d.n_h * d.d_h, d.d_h, w->ukt, d.d_h, (long long)d.d_c * d.d_h, T_,
+                     d.d_c, d.d_h, d.n_h, epi, ws, P.base, st)))
+      return cuda_status(e);
+  }
+  // (5) attention on the latent cache, (6) o_h = W_UV,h obar_h.
+  s = attend_ragged_impl(d, at<T>(ws, P.qabs), (long long)d.n_h * q_row, q_row, q_start, kv_len, page_table, B, T_,
+                         max_pages, num_pages, cache, at<T>(ws, P.obar), nullptr, at<char>(ws, P.ragged), P.attend,
+                         at<int>(ws, P.base.hdr), true, st);
+  if (s != MLA_OK) return s;
+  EpiStore<float> epi{out, (long long)d.n_h * d.d_v, d.d_v, 1.f};
+  return cuda_status(gemm<T>(at<T>(ws, P.obar), (long long)d.n_h * d.d_c, d.d_c, w->uv, d.d_c,
+                             (long long)d.d_v * d.d_c, T_, d.d_v, d.d_c, d.n_h, epi, ws, P.base, st));
 }
 
 }  // namespace
@@ -297,7 +370,39 @@ mla_status mla_attend_ragged(const mla_dims* dims, const void* q, int64_t q_toke
   if (workspace_bytes < P.total) return MLA_ERR_WORKSPACE;
   g_launches = 0;
   return attend_ragged_impl(d, q, q_token_stride, q_head_stride, q_start, kv_len, page_table, B, T, max_pages, num_pages,
-                            cache, out, lse, workspace, P, stream);
+                            cache, out, lse, workspace, P, at<int>(workspace, P.hdr), false, stream);
+}
+
+size_t mla_ragged_step_workspace_bytes(const mla_dims* dims, int B, int T) {
+  if (check_ragged(dims, B, T) != MLA_OK) return 0;
+  return make_ragged_step_plan(*dims, B, T).total;
+}
+
+mla_status mla_ragged_step(const mla_weights* w, const void* h, const int32_t* q_start, const int32_t* kv_len,
+                           const int32_t* seq_idx, const int32_t* pos, const int32_t* page_table, int max_pages,
+                           int num_pages, void* cache, float* out, int B, int T, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+  if (!w) return MLA_ERR_INVALID_ARG;
+  mla_status s = check_ragged(&w->d, B, T);
+  if (s != MLA_OK) return s;
+  if (max_pages <= 0 || num_pages <= 0 || num_pages > INT_MAX / 64 || max_pages > INT_MAX / 64)
+    return MLA_ERR_INVALID_ARG;
+  if (T == 0) return MLA_OK;
+  if (!h || !q_start || !kv_len || !seq_idx || !pos || !page_table || !cache || !out || !workspace)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256) || !aligned(h, 16) || !aligned(cache, 16) || !aligned(out, 16) ||
+      !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(seq_idx, 4) || !aligned(pos, 4) ||
+      !aligned(page_table, 4))
+    return MLA_ERR_INVALID_ARG;
+  const RaggedStepPlan P = make_ragged_step_plan(w->d, B, T);
+  if (workspace_bytes < P.total) return MLA_ERR_WORKSPACE;
+  s = begin_call(workspace, stream, P.base);
+  if (s != MLA_OK) return s;
+  if (w->d.dtype == MLA_BF16)
+    return ragged_step_impl<__nv_bfloat16>(w, h, q_start, kv_len, seq_idx, pos, page_table, B, T, max_pages, num_pages,
+                                           cache, out, workspace, P, stream);
+  return ragged_step_impl<float>(w, h, q_start, kv_len, seq_idx, pos, page_table, B, T, max_pages, num_pages, cache,
+                                 out, workspace, P, stream);
 }
 
 }  // extern "C"

@@ -51,6 +51,7 @@ struct RaggedSchedArgs {
   const int32_t* q_start;  // [B+1]
   const int32_t* kv_len;   // [B]
   int B, T, n_h, rows, W, max_pages, r_max, block_tiles;
+  int keep_err;            // the error word is an earlier launch's too: do not zero it
   RaggedSched s;
   int* err;
   int smem_ints;           // words of dynamic shared memory
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   sm100::pdl_wait();
   sm100::pdl_trigger();
   if (tid == 0) {
-    *a.err = 0;
+    if (!a.keep_err) *a.err = 0;
     *a.s.split_n = 0;
   }
   __syncthreads();

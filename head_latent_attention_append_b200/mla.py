@@ -29,6 +29,7 @@ EXPORTED = [
     "mla_selftest_wait_timeout", "mla_prefill_materialised_workspace_bytes", "mla_prefill_materialised",
     "mla_decode_step_workspace_bytes", "mla_decode_step", "mla_plan_step", "mla_append_normed",
     "mla_query_norm_rope", "mla_attend_ragged_workspace_bytes", "mla_attend_ragged",
+    "mla_ragged_step_workspace_bytes", "mla_ragged_step",
 ]
 APPEND_NOALLOC_MAX_T = 256
 
@@ -88,6 +89,8 @@ def _load():
         "mla_append_normed": (S, [D, P, L, P, P, L, P, P, L, F, P, P, P, I, I, P, P]),
         "mla_query_norm_rope": (S, [D, P, L, P, F, P, P, L, L, P, L, L, I, P]),
         "mla_attend_ragged_workspace_bytes": (Z, [D, I, I]),
+        "mla_ragged_step_workspace_bytes": (Z, [D, I, I]),
+        "mla_ragged_step": (S, [P, P, P, P, P, P, P, I, I, P, P, I, I, P, Z, P]),
         "mla_attend_ragged": (S, [D, P, L, L, P, P, P, I, I, P, P, P, I, I, P, Z, P]),
     }
     for name, (res, args) in sig.items():
@@ -377,6 +380,19 @@ def attend_ragged(dims: Dims, q, q_start, kv_len, page_table, cache, out, lse, w
             ("cache", cache, dt, (None, dims.page_size, row), True), ("out", out, dt, (T, n_h, dims.d_c), True),
             ("lse", lse, torch.float32, (T, n_h), True),
             ("workspace", workspace, workspace.dtype, tuple(workspace.shape), True)))
+
+
+def ragged_step_workspace_bytes(dims: Dims, B: int, T: int) -> int:
+    return lib.mla_ragged_step_workspace_bytes(ctypes.byref(dims), B, T)
+
+
+def ragged_step(w: Weights, h, q_start, kv_len, seq_idx, pos, page_table, num_pages: int, cache, out, workspace,
+                stream=None):
+    """Append and attention of every request's new tokens, from hidden states (include/mla.h)."""
+    _check("mla_ragged_step", lib.mla_ragged_step(
+        w.handle, _ptr(h), _ptr(q_start), _ptr(kv_len), _ptr(seq_idx), _ptr(pos), _ptr(page_table), page_table.shape[1],
+        num_pages, _ptr(cache), _ptr(out), kv_len.shape[0], h.shape[0], _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def selftest_wait_timeout(workspace, limit_us: int, stream=None):

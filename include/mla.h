@@ -316,7 +316,8 @@ mla_status mla_prefill_materialised(const mla_weights* w, const void* h, const i
  *                        position part
  *   mla_attend_ragged    absorbed attention of all new tokens
  *
- * They take mla_dims instead of a weights handle.  Tensors that are read and
+ * and mla_ragged_step runs a whole step of an unnormalised model on the last.
+ * The four take mla_dims instead of a weights handle.  Tensors that are read and
  * tensors that are written must not overlap unless said otherwise.
  *
  * Row convention: the new tokens of request b are rows q_start[b] ..
@@ -401,6 +402,23 @@ mla_status mla_attend_ragged(const mla_dims* dims, const void* q, int64_t q_toke
                              const int32_t* page_table, int max_pages, int num_pages,
                              const void* cache, void* out, float* lse, int B, int T,
                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Ragged step.  From hidden states to outputs for the new tokens of any number
+ * of requests: what mla_decode_step does for one number of new tokens per
+ * sequence and mla_prefill from position 0.  h [T, d_model], seq_idx [T] and
+ * pos [T] as mla_plan_step leaves them (with rows behind the last token: seq_idx
+ * -1), q_start [B+1] and kv_len [B] likewise; appends c = W_DKV h and
+ * RoPE(W_KR h) of every token to the cache, then writes out [T, n_h, d_v] (fp32)
+ * = W_UV,h sum_k alpha_k c_k with the queries of mla_decode (unnormalised, as
+ * there).  Rows of no request are unspecified in out.  Errors as
+ * mla_append_latent and mla_attend_ragged report them.  Workspace:
+ * mla_ragged_step_workspace_bytes, for at least this B and T. */
+size_t mla_ragged_step_workspace_bytes(const mla_dims* dims, int B, int T);
+mla_status mla_ragged_step(const mla_weights* w, const void* h, const int32_t* q_start,
+                           const int32_t* kv_len, const int32_t* seq_idx, const int32_t* pos,
+                           const int32_t* page_table, int max_pages, int num_pages, void* cache,
+                           float* out, int B, int T, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Status.

@@ -583,3 +583,67 @@ def test_a_ragged_step_from_lengths_to_outputs(mla):
                 assert (out[row + i].double() - ref).norm() <= 6 * U["bf16"] * ref.norm()
             past[b] += new[b]
             row += new[b]
+
+
+@pytest.mark.parametrize("dtype,dims_", [("bf16", (16, 128, 128, 256, 32, 512, 0)), ("bf16", (128, 64, 64, 512, 64, 256, 128)),
+                                         ("f32", (4, 32, 32, 64, 16, 128, 0)), ("f32", (3, 16, 24, 40, 6, 64, 48))])
+def test_ragged_step_matches_oracle_over_several_steps(mla, dtype, dims_):
+    """Requests that grow by different numbers of tokens, planned on the GPU, against the oracle's decode of each."""
+    import oracle as O
+    from head_latent_attention_append_b200 import synth, workload
+    n_h, d_h, d_v, d_c, d_r, d_model, d_cq = dims_
+    wl = synth.Workload("ragged", 21, n_h, d_h, d_v, d_c, d_r, d_model, d_cq, dtype, "decode", 5, 1, 0)
+    hw = synth.make_weights(wl, 5)
+    weights = mla.Weights(workload.dims_of(wl), workload.upload_weights(wl, hw, torch.device(DEV)))
+    odims, ow = O.Dims(n_h, d_h, d_v, d_c, d_r, d_model, d_cq, wl.rope_base), O.Weights(**hw.as_dict())
+    steps = [[70, 1, 0, 130, 5], [1, 3, 64, 1, 1], [0, 2, 1, 0, 40]]
+    H = [synth.make_hidden(wl, b, sum(s[b] for s in steps), 5) for b in range(5)]
+    num_pages, width = 24, 5
+    table = torch.full((5, width), -1, dtype=torch.int32, device=DEV)
+    free = torch.randperm(num_pages, generator=gen(2), device=DEV).to(torch.int32)
+    cache = torch.full((num_pages, 64, d_c + d_r), float("nan"), dtype=DT[dtype], device=DEV)
+    taken, past = 0, [0] * 5
+    for new in steps:
+        total, rows = sum(new), sum(new) + 4
+        q_start, kv_len, seq, pos = i32([0] * 6), i32([0] * 5), i32([0] * rows), i32([0] * rows)
+        counts, slot = i32([0] * 3), torch.zeros(rows, dtype=torch.int64, device=DEV)
+        mla.plan_step(i32(new), i32(past), free[taken:], table, num_pages, q_start, kv_len, seq, pos, slot, counts)
+        h = torch.from_numpy(np.concatenate([H[b][past[b]:past[b] + new[b]] for b in range(5)]
+                                            + [np.zeros((4, d_model), np.float32)])).to(DEV, DT[dtype])
+        out = torch.empty(rows, n_h, d_v, device=DEV)
+        ws = torch.empty(mla.ragged_step_workspace_bytes(weights.dims, 5, rows), dtype=torch.uint8, device=DEV)
+        mla.ragged_step(weights, h, q_start, kv_len, seq, pos, table, num_pages, cache, out, ws)
+        assert mla.get_error(ws) == mla.MLA_OK
+        taken += int(counts[2])
+        got, row = out.cpu().numpy(), 0
+        for b in range(5):
+            past[b] += new[b]
+            if new[b]:
+                ref = O.mla_decode(odims, ow, H[b][:past[b]], new[b])
+                # The bounds of the library's other paths (their intermediates are rounded alike).
+                err = np.abs(got[row:row + new[b]] - ref).max() / np.abs(ref).max()
+                assert err <= {"f32": 1e-4, "bf16": 2e-2}[dtype], (b, err)
+            row += new[b]
+
+
+def test_ragged_step_reports_rows_that_belong_nowhere(mla):
+    from head_latent_attention_append_b200 import synth, workload
+    wl = synth.Workload("ragged", 22, 4, 32, 32, 64, 16, 128, 0, "f32", "decode", 2, 1, 0)
+    weights = mla.Weights(workload.dims_of(wl), workload.upload_weights(wl, synth.make_weights(wl, 5), torch.device(DEV)))
+    h = torch.zeros(3, 128, device=DEV)
+    cache, out = torch.zeros(4, 64, 80, device=DEV), torch.empty(3, 4, 32, device=DEV)
+    ws = torch.empty(mla.ragged_step_workspace_bytes(weights.dims, 2, 3), dtype=torch.uint8, device=DEV)
+
+    def run(seq, pos, kv, table):
+        mla.ragged_step(weights, h, i32([0, 2, 3]), i32(kv), i32(seq), i32(pos), i32(table), 4, cache, out, ws)
+        return mla.get_error(ws)
+
+    good = [[0, 1], [2, 3]]
+    assert run([0, 0, 1], [0, 1, 0], [2, 1], good) == 0
+    assert run([0, 0, -1], [0, 1, 0], [2, 1], good) == 0          # a row of no request
+    assert run([0, 0, 2], [0, 1, 0], [2, 1], good) == -5
+    assert run([0, 0, -2], [0, 1, 0], [2, 1], good) == -5
+    assert run([0, 0, 1], [0, 128, 0], [2, 1], good) == -5
+    assert run([0, 0, 1], [0, 1, 0], [2, 129], good) == -5
+    assert run([0, 0, 1], [0, 1, 0], [2, 1], [[0, 1], [9, 3]]) == -5
+    assert run([0, 0, 1], [0, 1, 0], [2, 1], good) == 0

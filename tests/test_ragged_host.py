@@ -137,3 +137,13 @@ def test_the_binding_refuses_tensors_it_could_not_pass_on(mla):
                     ("slot", pos), ("counts", v), ("free_pages", slot), ("new_len", v)):
         with pytest.raises(mla.MlaError):
             mla.plan_step(**{**ok, name: t})
+
+
+def test_ragged_step_refusals_and_sizes(mla):
+    d = dims(mla)
+    need = mla.ragged_step_workspace_bytes(d, 4, 70)
+    assert need >= mla.attend_ragged_workspace_bytes(d, 4, 70) + 2 * 70 * 16 * (128 + 288 + 256) + 2 * 70 * 1536
+    assert mla.ragged_step_workspace_bytes(d, 0, 70) == 0 and mla.ragged_step_workspace_bytes(d, 4, -1) == 0
+    assert mla.ragged_step_workspace_bytes(dims(mla, rope_key_per_head=1, d_c=128), 4, 70) == 0
+    # A null handle is refused before anything else is looked at.
+    assert mla.lib.mla_ragged_step(None, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 9, FAKE, FAKE, 4, 70, FAKE, need, None) == INVALID
