@@ -134,7 +134,7 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
                             tc ? kBlockTilesTc : kBlockTilesSimt, keep_err, S, err, ints};
     if ((e = set_smem_once(ragged_sched_kernel, sizeof(int) * (size_t)kRaggedSmemInts))) return cuda_status(e);
     ++g_launches;
-    if ((e = launch_pdl(ragged_sched_kernel, dim3(1), dim3(P.r_max > 1024 ? 1024 : 256), sizeof(int) * (size_t)ints, st, a)))
+    if ((e = launch_pdl(ragged_sched_kernel, dim3(1), dim3(P.r_max <= 256 ? 256 : P.r_max <= kSchedSmall ? kSchedSmall : 1024), sizeof(int) * (size_t)ints, st, a)))
       return cuda_status(e);
   }
   ++g_launches;
@@ -258,7 +258,7 @@ mla_status mla_plan_step(const int32_t* new_len, const int32_t* past_len, int B,
       !aligned(pos, 4) || !aligned(counts, 4) || !aligned(device_error, 4))
     return MLA_ERR_INVALID_ARG;
   // Sums and positions in 32 bits.
-  if (B > step::PLAN_MAX_B || rows == INT_MAX || n_free == INT_MAX || max_pages > INT_MAX / 64 - 1)
+  if (B > step::PLAN_MAX_B || rows > (1 << 30) || n_free > (1 << 30) || max_pages > INT_MAX / 64 - 1)
     return MLA_ERR_UNSUPPORTED;
   const step::PlanArgs a{new_len, past_len, free_pages, page_table, q_start, kv_len,    seq_idx, pos,
                          slot,    counts,   device_error, B,        n_free,  max_pages, num_pages, rows};

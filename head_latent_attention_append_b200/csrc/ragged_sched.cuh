@@ -19,7 +19,7 @@
 namespace mla {
 
 constexpr int kRaggedMaxB = 16384;      // requests whose row-block offsets sit in shared memory
-constexpr int kRaggedSmemInts = 56000;  // 4-byte words of shared memory the schedule may use
+constexpr int kRaggedSmemInts = 47000;  // 4-byte words of dynamic shared memory the schedule may use
 
 struct __align__(16) RSeg {
   int row0, nrows;  // the row block's rows
@@ -90,9 +90,87 @@ __device__ __noinline__ long long ragged_scan(int* data, int n) {
   return total;
 }
 
+// Exclusive scan of one value per thread (each below 2^25), with one barrier.
+// `words`: two per warp, not used by another scan since the last barrier.
+__device__ __forceinline__ int block_scan_once(int v, long long* words, long long* total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) words[wid] = x;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll 8
+  for (int i = 0; i < warps; ++i) {
+    const long long t = words[i];
+    before += i < wid ? t : 0;
+    all += t;
+  }
+  *total = all;
+  return (int)before + x - v;
+}
+
+// Where row block `i` of the request whose rows start at token s0, end at s1
+// and see L keys lies.
+__device__ __forceinline__ RSeg ragged_block(const RaggedSchedArgs& a, int b, int i, int s0, int s1, int L) {
+  RSeg g;
+  g.seq = b;
+  g.row0 = s0 * a.n_h + i * a.rows;
+  g.nrows = min(a.rows, s1 * a.n_h - g.row0);
+  g.base = L - s1;
+  g.nkeys = max(0, g.base + (g.row0 + g.nrows - 1) / a.n_h + 1);
+  g.kmin = max(0, g.base + g.row0 / a.n_h + 1);
+  return g;
+}
+__device__ __forceinline__ int ragged_tiles(const RSeg& g) { return max(1, (g.nkeys + 63) >> 6); }
+
+// The shares: worker w's starts at tile w len + min(w, rest).
+struct RaggedShares {
+  int total, W, len, rest, longer, block_tiles;
+  __device__ __forceinline__ RaggedShares(int total_, int workers, int tiles)
+      : total(total_), W(min(workers, total_)), block_tiles(tiles) {  // every share has at least one tile
+    len = total / W;
+    rest = total - len * W;
+    longer = rest * (len + 1);
+  }
+  __device__ __forceinline__ int share(int w) const { return w * len + min(w, rest); }
+  __device__ __forceinline__ int owner(int x) const {  // the worker whose share holds tile x
+    const bool in = x < longer;
+    return (in ? 0 : rest) + (x - (in ? 0 : longer)) / (in ? len + 1 : len);
+  }
+  // Segment s, piece k of `pieces` of the row block g whose (weighted) tiles
+  // are [v0, v1), owned by worker w; `before`: the worker of segment s - 1.
+  __device__ __forceinline__ void emit(const RaggedSchedArgs& a, RSeg g, int s, int k, int pieces, int v0, int v1, int w,
+                                       int before, bool last) const {
+    const int start = v0 + block_tiles;
+    g.t_lo = max(share(w) - start, 0);
+    g.t_hi = min(share(w + 1), v1) - start;
+    // Only the first and the last segment of a worker can be pieces.
+    g.slot = pieces == 1 ? -1 : ragged_slot(w - k, k);
+    g.pad[0] = g.pad[1] = g.pad[2] = 0;
+    a.s.segs[s] = g;
+    if (before < w) a.s.first[w] = g;
+    for (int v = before + 1; v <= w; ++v) a.s.worker_seg[v] = s;  // shares without a segment start here too
+    if (last)
+      for (int v = w + 1; v <= a.W; ++v) a.s.worker_seg[v] = s + 1;
+    if (k == 0 && pieces > 1) a.s.split[atomicAdd(a.s.split_n, 1)] = make_int4(g.row0, g.nrows, w, pieces);
+  }
+};
+
+// Up to kSchedSmall requests and row blocks take the short way, one per thread
+// with one barrier per sum: the schedule stands at the head of a call that may
+// take 15 us, and cost 6 of them the long way.
+constexpr int kSchedSmall = 512;
+
 __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArgs a) {
   extern __shared__ int rs_smem[];
-  int* const bs = rs_smem;  // [B+1] first row block of each request
+  __shared__ long long words[3][kSchedSmall / 32];
+  __shared__ int bs_s[kSchedSmall + 1], vs_s[kSchedSmall + 1], pc_s[kSchedSmall + 1], wf_s[kSchedSmall];
+  __shared__ int4 req[kSchedSmall];
+  __shared__ RSeg blocks[kSchedSmall];
   const int tid = threadIdx.x, nt = blockDim.x;
   sm100::pdl_wait();
   sm100::pdl_trigger();
@@ -100,87 +178,114 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
     if (!a.keep_err) *a.err = 0;
     *a.s.split_n = 0;
   }
-  __syncthreads();
   // Starts that leave [0, T] or decrease leave nothing to compute; a length
   // outside its page table is clamped.
-  int bad = 0;
+  const bool small = a.B <= nt && nt <= kSchedSmall;
+  int* const bs = small ? bs_s : rs_smem;  // [B+1] first row block of each request
+  int bad = 0, range = 0;
   for (int b = tid; b < a.B; b += nt) {
-    const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
-    if (s0 < 0 || s1 < s0 || s1 > a.T) bad = 1;
-    const int n = bad ? 0 : s1 - s0, L = a.kv_len[b];
-    if (n > 0 && (L < 0 || L > a.max_pages * 64LL)) flag_error(a.err, kErrBounds);
-    bs[b] = (int)(((long long)n * a.n_h + a.rows - 1) / a.rows);
+    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], L = a.kv_len[b];
+    const bool ok = s0 >= 0 && s1 >= s0 && s1 <= a.T;
+    const long long most = a.max_pages * 64LL;
+    if (!ok) bad = 1;
+    if (ok && s1 > s0 && (L < 0 || L > most)) range = 1;
+    bs[b] = ok ? (int)(((long long)(s1 - s0) * a.n_h + a.rows - 1) / a.rows) : 0;
+    if (small) req[b] = make_int4(s0, s1, (int)min(max((long long)L, 0LL), most), 0);
   }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) flag_error(a.err, kErrBounds);
+  const int none = __syncthreads_or(bad);
+  if (range || (none && tid == 0)) flag_error(a.err, kErrBounds);
+  if (none) {
     for (int w = tid; w <= a.W; w += nt) a.s.worker_seg[w] = 0;
     return;
   }
-  const int R = (int)ragged_scan(bs, a.B);  // <= r_max: the starts are in order
-  if (tid == 0) bs[a.B] = R;
+
+  if (small) {
+    long long sum;
+    const int n_blocks = tid < a.B ? bs[tid] : 0, first_rb = block_scan_once(n_blocks, words[0], &sum);
+    const int R = (int)sum;  // <= r_max: the starts are in order
+    if (R <= nt) {
+      if (tid < a.B) bs[tid] = first_rb;
+      __syncthreads();
+      const bool mine = tid < R;
+      RSeg g{};
+      int v = 0;
+      if (mine) {
+        const int b = find_le(bs, a.B, tid);
+        const int4 q = req[b];
+        g = ragged_block(a, b, tid - bs[b], q.x, q.y, q.z);
+        v = ragged_tiles(g) + a.block_tiles;
+        blocks[tid] = g;
+      }
+      const int v0 = block_scan_once(v, words[1], &sum);
+      if (R == 0 || sum > 0x7fffffffLL) {
+        if (tid == 0 && R > 0) flag_error(a.err, kErrBounds);
+        for (int w = tid; w <= a.W; w += nt) a.s.worker_seg[w] = 0;
+        return;
+      }
+      const RaggedShares sh((int)sum, a.W, a.block_tiles);
+      int pieces = 0;
+      if (mine) {
+        const int w0 = sh.owner(v0 + a.block_tiles);
+        pieces = sh.owner(v0 + v - 1) - w0 + 1;
+        wf_s[tid] = w0;
+        vs_s[tid] = v0;
+      }
+      const int s0 = block_scan_once(pieces, words[2], &sum);
+      if (mine) pc_s[tid] = s0;
+      const int nseg = (int)sum;
+      if (tid == 0) {
+        pc_s[R] = nseg;
+        vs_s[R] = sh.total;
+      }
+      __syncthreads();
+      for (int s = tid; s < nseg; s += nt) {
+        const int rb = find_le(pc_s, R, s), k = s - pc_s[rb], w = wf_s[rb] + k;
+        const int before = k > 0 ? w - 1 : (rb > 0 ? wf_s[rb - 1] + s - pc_s[rb - 1] - 1 : -1);
+        sh.emit(a, blocks[rb], s, k, pc_s[rb + 1] - pc_s[rb], vs_s[rb], vs_s[rb + 1], w, before, s == nseg - 1);
+      }
+      return;
+    }
+    // Many row blocks of few requests: the offsets go where the long way has them.
+    for (int b = tid; b < a.B; b += nt) rs_smem[b] = bs_s[b];
+    __syncthreads();
+  }
+
+  int* const off = rs_smem;
+  const int R = (int)ragged_scan(off, a.B);  // <= r_max
+  if (tid == 0) off[a.B] = R;
   const bool in_smem = a.B + 1 + 3 * (R + 1) <= a.smem_ints;
-  int* const vs = in_smem ? bs + a.B + 1 : a.s.vs;
+  int* const vs = in_smem ? off + a.B + 1 : a.s.vs;
   int* const pc = in_smem ? vs + R + 1 : a.s.pc;
   int* const wf = in_smem ? pc + R + 1 : a.s.wf;
   __syncthreads();
-
   auto block = [&](int rb) {
-    RSeg g;
-    const int b = find_le(bs, a.B, rb);
-    const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
-    const int L = (int)min(max((long long)a.kv_len[b], 0LL), a.max_pages * 64LL);
-    g.seq = b;
-    g.row0 = s0 * a.n_h + (rb - bs[b]) * a.rows;
-    g.nrows = min(a.rows, s1 * a.n_h - g.row0);
-    g.base = L - s1;
-    g.nkeys = max(0, g.base + (g.row0 + g.nrows - 1) / a.n_h + 1);
-    g.kmin = max(0, g.base + g.row0 / a.n_h + 1);
-    return g;
+    const int b = find_le(off, a.B, rb);
+    return ragged_block(a, b, rb - off[b], a.q_start[b], a.q_start[b + 1],
+                        (int)min(max((long long)a.kv_len[b], 0LL), a.max_pages * 64LL));
   };
-  for (int rb = tid; rb < R; rb += nt) vs[rb] = max(1, ceil_div(block(rb).nkeys, 64)) + a.block_tiles;
+  for (int rb = tid; rb < R; rb += nt) vs[rb] = ragged_tiles(block(rb)) + a.block_tiles;
   __syncthreads();
-  const long long total64 = ragged_scan(vs, R);
-  if (R == 0 || total64 > 0x7fffffffLL) {
+  const long long total = ragged_scan(vs, R);
+  if (R == 0 || total > 0x7fffffffLL) {
     if (tid == 0 && R > 0) flag_error(a.err, kErrBounds);
     for (int w = tid; w <= a.W; w += nt) a.s.worker_seg[w] = 0;
     return;
   }
-  const int total = (int)total64;
-  if (tid == 0) vs[R] = total;
-  const int W = min(a.W, total);  // every worker's share has at least one tile
-  // Worker w's share starts at tile w len + min(w, rest).
-  const int len = total / W, rest = total - len * W, longer = rest * (len + 1);
-  auto share = [&](int w) { return w * len + min(w, rest); };
-  auto owner = [&](int x) {  // the worker whose share holds tile x
-    const bool in = x < longer;
-    return (in ? 0 : rest) + (x - (in ? 0 : longer)) / (in ? len + 1 : len);
-  };
+  if (tid == 0) vs[R] = (int)total;
+  const RaggedShares sh((int)total, a.W, a.block_tiles);
   __syncthreads();
   for (int rb = tid; rb < R; rb += nt) {
-    wf[rb] = owner(vs[rb] + a.block_tiles);
-    pc[rb] = owner(vs[rb + 1] - 1) - wf[rb] + 1;
+    wf[rb] = sh.owner(vs[rb] + a.block_tiles);
+    pc[rb] = sh.owner(vs[rb + 1] - 1) - wf[rb] + 1;
   }
   __syncthreads();
   const int nseg = (int)ragged_scan(pc, R);  // <= R + W
   if (tid == 0) pc[R] = nseg;
   __syncthreads();
   for (int s = tid; s < nseg; s += nt) {
-    const int rb = find_le(pc, R, s), k = s - pc[rb], pieces = pc[rb + 1] - pc[rb];
-    const int start = vs[rb] + a.block_tiles, w = wf[rb] + k;
-    RSeg g = block(rb);
-    g.t_lo = max(share(w) - start, 0);
-    g.t_hi = min(share(w + 1), vs[rb + 1]) - start;
-    // Only the first and the last segment of a worker can be pieces.
-    g.slot = pieces == 1 ? -1 : ragged_slot(w - k, k);
-    g.pad[0] = g.pad[1] = g.pad[2] = 0;
-    a.s.segs[s] = g;
-    // The previous segment's worker; the ones behind it, up to this one, start here.
+    const int rb = find_le(pc, R, s), k = s - pc[rb], w = wf[rb] + k;
     const int before = k > 0 ? w - 1 : (rb > 0 ? wf[rb - 1] + s - pc[rb - 1] - 1 : -1);
-    if (before < w) a.s.first[w] = g;
-    for (int v = before + 1; v <= w; ++v) a.s.worker_seg[v] = s;
-    if (s == nseg - 1)
-      for (int v = w + 1; v <= a.W; ++v) a.s.worker_seg[v] = nseg;
-    if (k == 0 && pieces > 1) a.s.split[atomicAdd(a.s.split_n, 1)] = make_int4(g.row0, g.nrows, w, pieces);
+    sh.emit(a, block(rb), s, k, pc[rb + 1] - pc[rb], vs[rb], vs[rb + 1], w, before, s == nseg - 1);
   }
 }
 

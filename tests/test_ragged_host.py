@@ -39,7 +39,7 @@ def test_plan_refusals(mla):
     for bad in (dict(B=0), dict(B=-1), dict(n_free=-1), dict(max_pages=0), dict(num_pages=0), dict(rows=-1),
                 dict(slot=FAKE + 4), dict(err=FAKE + 1)):
         assert call(f, ok, **bad) == INVALID, bad
-    for bad in (dict(B=16385), dict(rows=2 ** 31 - 1), dict(n_free=2 ** 31 - 1), dict(max_pages=2 ** 25)):
+    for bad in (dict(B=16385), dict(rows=2 ** 31 - 1), dict(rows=2 ** 30 + 1), dict(n_free=2 ** 31 - 1), dict(max_pages=2 ** 25)):
         assert call(f, ok, **bad) == UNSUPPORTED, bad
 
 
