@@ -318,7 +318,9 @@ mla_status mla_prefill_materialised(const mla_weights* w, const void* h, const i
  *
  * and mla_ragged_step runs a whole step of an unnormalised model on the last.
  * The four take mla_dims instead of a weights handle.  Tensors that are read and
- * tensors that are written must not overlap unless said otherwise.
+ * tensors that are written must not overlap unless said otherwise.  All can be
+ * captured into a graph (after a first call outside one) and read their lengths,
+ * tables and positions on the device when they run.
  *
  * Row convention: the new tokens of request b are rows q_start[b] ..
  * q_start[b+1] - 1 of every packed tensor, and sit at positions
@@ -391,9 +393,10 @@ mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_st
  * nothing: zeros and -inf.  Rows outside [q_start[0], q_start[B]) are left as
  * they are.  Cache rows that no query sees may hold anything.  q_start that
  * decreases or leaves [0, T] computes nothing; a length outside
- * [0, max_pages*64] is clamped; a page id outside [0, num_pages) is read as
- * page 0; each sets MLA_ERR_DEVICE_BOUNDS in the workspace error word.
- * Deterministic.  One shared RoPE key and B <= 16384 (else
+ * [0, max_pages*64] counts as the nearest one, and the outputs of a request with
+ * a page id outside [0, num_pages) are unspecified; each sets
+ * MLA_ERR_DEVICE_BOUNDS in the workspace error word.  A NaN or infinity in a key
+ * that a query does not see does not reach it.  Deterministic.  One shared RoPE key and B <= 16384 (else
  * MLA_ERR_UNSUPPORTED).  Workspace: mla_attend_ragged_workspace_bytes, for at
  * least this B and T. */
 size_t mla_attend_ragged_workspace_bytes(const mla_dims* dims, int B, int T);

@@ -271,15 +271,13 @@ def test_norm_of_extreme_rows(mla, x):
         assert torch.isnan(y).all()
 
 
-QUERY_DIMS = [("bf16", 128, 128, 64), ("bf16", 16, 128, 32), ("bf16", 1, 8, 16), ("bf16", 5, 96, 48), ("bf16", 3, 1500, 16),
+QUERY_DIMS = [("bf16", 128, 128, 64), ("bf16", 16, 128, 32), ("bf16", 1, 8, 16), ("bf16", 5, 96, 48), ("bf16", 3, 1504, 16),
               ("f32", 4, 32, 16), ("f32", 3, 5, 2), ("f32", 2, 131, 62), ("f32", 128, 64, 64), ("f32", 1, 1028, 4)]
 
 
 @pytest.mark.parametrize("dtype,n_h,d_h,d_r", QUERY_DIMS)
 @pytest.mark.parametrize("T,form", [(1, "dense"), (9, "dense"), (9, "absorbed"), (9, "odd"), (9, "in place")])
 def test_query_norm_rope_matches_the_formula(mla, dtype, n_h, d_h, d_r, T, form):
-    if dtype == "bf16" and d_h % 8:
-        pytest.skip("bf16 dimensions are multiples of 8")
     g = gen(n_h + d_h)
     dims = dims_of(mla, dtype, n_h, d_h, 128, d_r)
     pad = 3 if form == "odd" else 0
@@ -647,3 +645,141 @@ def test_ragged_step_reports_rows_that_belong_nowhere(mla):
     assert run([0, 0, 1], [0, 1, 0], [2, 129], good) == -5
     assert run([0, 0, 1], [0, 1, 0], [2, 1], [[0, 1], [9, 3]]) == -5
     assert run([0, 0, 1], [0, 1, 0], [2, 1], good) == 0
+
+
+# --------------------------------------------------- sizes and uses at the edges
+@pytest.mark.parametrize("dtype,n_h,B,most", [("bf16", 16, 700, 3), ("f32", 4, 520, 2), ("bf16", 128, 40, 60), ("f32", 64, 40, 60)])
+def test_attend_ragged_schedules_of_many_requests_and_row_blocks(mla, dtype, n_h, B, most):
+    r = np.random.default_rng(B)
+    lens = [(int(n), int(n + p)) for n, p in zip(r.integers(0, most + 1, B), r.integers(0, 150, B))]
+    s = Step(mla, dtype, n_h, 128, 16, lens)
+    out, lse = s.run()
+    s.check(out, lse, only=list(r.choice(B, 12, replace=False)) + [0, B - 1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_ragged_schedule_that_does_not_fit_shared_memory(mla, dtype):
+    """16,000 requests of one token and 64 heads or more are more row blocks than the schedule keeps on chip."""
+    r = np.random.default_rng(7)
+    B, n_h = 16000, 128 if dtype == "bf16" else 64
+    lens = [(1, int(k)) for k in r.integers(1, 4, B)]
+    s = Step(mla, dtype, n_h, 128, 16, lens)
+    out, lse = s.run()
+    s.check(out, lse, only=list(r.choice(B, 30, replace=False)) + [0, B - 1])
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+def test_attend_ragged_offsets_past_32_bits(mla):
+    """Queries and outputs of more than 2^31 elements and a cache of more than 4 GiB."""
+    n_h, d_c, d_r = 128, 512, 64
+    dims = dims_of(mla, "bf16", n_h, 32, d_c, d_r)
+    B, n = 330, 100
+    T, num_pages = B * n, 70000
+    assert T * n_h * d_c > 2 ** 31 and num_pages * 64 * 576 * 2 > 2 ** 32
+    g = gen(3)
+    q = torch.empty(T, n_h, d_c + d_r, dtype=DT["bf16"], device=DEV)
+    q.normal_(generator=g)
+    cache = torch.full((num_pages, 64, d_c + d_r), float("nan"), dtype=DT["bf16"], device=DEV)
+    table = torch.randperm(num_pages, generator=g, device=DEV)[:2 * B].view(B, 2).to(torch.int32)
+    table[-1] = torch.tensor([num_pages - 1, num_pages - 2])
+    table[0, 0] = num_pages - 3
+    for b in range(B):
+        for j in range(2):
+            cache[table[b, j].long()].normal_(generator=g)
+    starts, kv = i32([n * b for b in range(B + 1)]), i32([n + 7] * B)
+    out = torch.empty(T, n_h, d_c, dtype=DT["bf16"], device=DEV)
+    lse = torch.empty(T, n_h, device=DEV)
+    ws = torch.empty(mla.attend_ragged_workspace_bytes(dims, B, T), dtype=torch.uint8, device=DEV)
+    mla.attend_ragged(dims, q, starts, kv, table, cache, out, lse, ws)
+    assert mla.get_error(ws) == 0
+    for t in (0, 99, T // 2, T - 101, T - 100, T - 1):
+        b, sees = t // n, 7 + t % n + 1
+        k = cache[table[b].long()].flatten(0, 1)[:sees].double()
+        a = q[t].double() @ k.t() / math.sqrt(32 + d_r)
+        alpha = torch.softmax(a, -1)
+        ref = alpha @ k[:, :d_c]
+        # As in Step.check: weights and output rounded once each, scores fp32 sums of 576 products.
+        ds = 576 * 2.0 ** -24 * float((q[t].double().abs() @ k.abs().t()).max()) / math.sqrt(32 + d_r)
+        tol = 1.05 * (U["bf16"] + 2 * ds + 1e-5) * (alpha @ k[:, :d_c].abs()) + U["bf16"] * ref.abs()
+        assert ((out[t].double() - ref).abs() <= tol).all(), t
+    assert torch.isfinite(lse).all()
+
+
+def test_norm_calls_offsets_past_32_bits(mla):
+    T, width = 300000, 8000                       # 2.4e9 elements of rows, of which slices are read
+    wide = torch.empty(T, width, dtype=DT["bf16"], device=DEV)
+    rows = torch.tensor([0, 1, T // 2, T - 2, T - 1], device=DEV)
+    wide[:, 7000:].normal_(generator=gen(4))
+    dims = dims_of(mla, "bf16", 2, 128, 512, 64, 16)
+    kv = wide[:, 7000:7576]
+    cache = torch.zeros(T // 64 + 1, 64, 576, dtype=DT["bf16"], device=DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    slot = torch.arange(T - 1, -1, -1, device=DEV)
+    ones = torch.ones(512, dtype=DT["bf16"], device=DEV)
+    mla.append_normed(dims, kv, ones, pos, slot, cache, 1e-6)
+    flat = cache.view(-1, 576)
+    close_norm(flat[slot[rows], :512], rms64(kv[rows, :512], ones, 1e-6), "bf16", 512)
+    close_turn(flat[slot[rows], 512:], turn64(kv[rows, 512:], pos[rows]), kv[rows, 512:], "bf16")
+    q = torch.as_strided(wide, (T, 2, 192), (width, 192, 1), 7600)
+    qc, qr = torch.as_strided(wide, (T, 2, 128), (width, 128, 1), 0), torch.as_strided(wide, (T, 2, 64), (width, 64, 1), 256)
+    mla.query_norm_rope(dims, q, ones[:128], pos, qc, qr, 1e-6)
+    close_norm(qc[rows], rms64(q[rows][..., :128], ones[:128], 1e-6), "bf16", 128)
+    close_turn(qr[rows], turn64(q[rows][..., 128:], pos[rows]), q[rows][..., 128:], "bf16")
+
+
+def test_calls_on_two_streams_at_once(mla):
+    """Each with its own workspace; the norm and plan calls have none."""
+    a = Step(mla, "bf16", 16, 256, 32, [(40, 3000), (3, 500)], seed=1)
+    b = Step(mla, "bf16", 16, 256, 32, [(1, 2000)] * 20, seed=2)
+    want = [a.run(), b.run()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(6):
+        for i, s in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(s.run())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_a_whole_step_in_one_graph(mla):
+    """Plan to attention captured once and replayed with other lengths."""
+    n_h, d_c, d_r, B, rows, num_pages = 16, 256, 32, 3, 80, 12
+    dims = dims_of(mla, "bf16", n_h, 32, d_c, d_r)
+    g = gen(9)
+    kv, q = randn(g, rows, d_c + d_r, dtype=DT["bf16"]), randn(g, rows, n_h, 32 + d_r, dtype=DT["bf16"])
+    absorbed = randn(g, rows, n_h, d_c + d_r, dtype=DT["bf16"])
+    gk = torch.ones(d_c, dtype=DT["bf16"], device=DEV)
+    new, past, free = i32([5, 1, 30]), i32([0, 0, 0]), torch.arange(num_pages, dtype=torch.int32, device=DEV)
+    table = torch.full((B, 4), -1, dtype=torch.int32, device=DEV)
+    q_start, kv_len, seq, pos = i32([0] * 4), i32([0] * 3), i32([0] * rows), i32([0] * rows)
+    slot, counts = torch.zeros(rows, dtype=torch.int64, device=DEV), i32([0] * 3)
+    cache = torch.zeros(num_pages, 64, d_c + d_r, dtype=DT["bf16"], device=DEV)
+    qc, out = torch.empty(rows, n_h, 32, dtype=DT["bf16"], device=DEV), torch.empty(rows, n_h, d_c, dtype=DT["bf16"], device=DEV)
+    ws = torch.empty(mla.attend_ragged_workspace_bytes(dims, B, rows), dtype=torch.uint8, device=DEV)
+
+    def step():
+        mla.plan_step(new, past, free, table, num_pages, q_start, kv_len, seq, pos, slot, counts)
+        mla.append_normed(dims, kv, gk, pos, slot, cache)
+        mla.query_norm_rope(dims, q, None, pos, qc, absorbed[..., d_c:])
+        mla.attend_ragged(dims, absorbed, q_start, kv_len, table, cache, out, None, ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lens in ([5, 1, 30], [64, 1, 15], [1, 1, 1], [0, 80, 0], [2, 70, 40]):
+        new.copy_(i32(lens))
+        table.fill_(-1)
+        out.fill_(7)
+        graph.replay()
+        got, rows_used = out.clone(), int(counts[1])
+        assert rows_used == (72 if lens == [2, 70, 40] else sum(lens))      # the last request does not fit
+        out.fill_(7)
+        step()
+        assert torch.equal(got, out) and (out[rows_used:] == 7).all() and torch.isfinite(out.float()).all()
+        assert mla.get_error(ws) == 0
