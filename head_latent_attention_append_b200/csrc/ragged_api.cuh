@@ -8,9 +8,11 @@ namespace {
 // CUDA cores.  The caps size the partial slots.
 constexpr int kRaggedPairs = 80, kRaggedCtas = 160;
 // What changing query rows costs a worker, in tiles of 64 keys: the next rows'
-// load and this block's output (about 6 us against 0.9 us a tile on the tensor
-// cores; small against a tile on the CUDA cores).
-constexpr int kBlockTilesTc = 6, kBlockTilesSimt = 1;
+// load and this block's output, about 6 us against 0.8 us a tile of a wide row
+// on the tensor cores; small against a tile on the CUDA cores.  Measured on
+// batches of 64 to 330 row blocks: with d_c = 512, 3, 6, 9 and 12 tiles gave 249,
+// 238, 232 and 234 us; with d_c = 256, 35.0, 33.5, 35.1 and 36.5.
+int block_tiles(const mla_dims& d) { return d.dtype == MLA_BF16 ? 3 + 3 * d.d_c / 256 : 1; }
 
 struct RaggedPlan {
   size_t hdr, vs, pc, wf, worker_seg, segs, first, split, part_o, part_ml, total;
@@ -131,7 +133,7 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
   {
     const int ints = (int)std::min<long long>(B + 1 + 3LL * (P.r_max + 1), kRaggedSmemInts);
     const RaggedSchedArgs a{q_start, kv_len, B, T, d.n_h, P.rows, W, max_pages, P.r_max,
-                            tc ? kBlockTilesTc : kBlockTilesSimt, keep_err, S, err, ints};
+                            block_tiles(d), keep_err, S, err, ints};
     if ((e = set_smem_once(ragged_sched_kernel, sizeof(int) * (size_t)kRaggedSmemInts))) return cuda_status(e);
     ++g_launches;
     if ((e = launch_pdl(ragged_sched_kernel, dim3(1), dim3(P.r_max <= 256 ? 256 : P.r_max <= kSchedSmall ? kSchedSmall : 1024), sizeof(int) * (size_t)ints, st, a)))
