@@ -15,7 +15,9 @@
 // four times above it and took 1.5 times as long), 8 x 4 NC in P V.  A small
 // batch is one tile per CTA and bound by latency, so all rows of a tile are
 // copied asynchronously at once, the next 32 keys while these are worked on
-// (where two buffers fit: rows of up to 432 values).
+// (where two buffers fit: rows of up to 432 values).  400 tokens of 16 heads over
+// up to 4000 keys run at 35 TFLOP/s; 39 tokens over up to 517 keys in 36 us, of
+// which one tile is 25.
 #pragma once
 #include "ragged_sched.cuh"
 
