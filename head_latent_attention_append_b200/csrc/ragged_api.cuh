@@ -49,6 +49,12 @@ mla_status check_ragged(const mla_dims* dims, int B, int T) {
   return MLA_OK;
 }
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na && nb && x < y + nb && y < x + na;
+}
+
 // RoPE frequencies as turns per position.
 step::Rope rope_table(const mla_dims& d) {
   static thread_local step::Rope last;
@@ -262,6 +268,15 @@ mla_status mla_plan_step(const int32_t* new_len, const int32_t* past_len, int B,
   // Sums and positions in 32 bits.
   if (B > step::PLAN_MAX_B || rows > (1 << 30) || n_free > (1 << 30) || max_pages > INT_MAX / 64 - 1)
     return MLA_ERR_UNSUPPORTED;
+  // Every CTA reads all lengths while others write: an output in their place
+  // (kv_len for past_len, say) would be read half updated.
+  const size_t i32 = sizeof(int32_t), nb = B * i32, nr = rows * i32;
+  const struct { const void* p; size_t n; } in[] = {{new_len, nb}, {past_len, nb}, {free_pages, n_free * i32}},
+      out[] = {{page_table, nb * (size_t)max_pages}, {q_start, nb + i32}, {kv_len, nb}, {seq_idx, nr}, {pos, nr},
+               {slot, 2 * nr}, {counts, 3 * i32}};
+  for (const auto& x : in)
+    for (const auto& y : out)
+      if (overlap(x.p, x.n, y.p, y.n)) return MLA_ERR_INVALID_ARG;
   const step::PlanArgs a{new_len, past_len, free_pages, page_table, q_start, kv_len,    seq_idx, pos,
                          slot,    counts,   device_error, B,        n_free,  max_pages, num_pages, rows};
   const size_t sm = sizeof(uint32_t) * 2 * ((size_t)B + 1);
@@ -368,6 +383,9 @@ mla_status mla_attend_ragged(const mla_dims* dims, const void* q, int64_t q_toke
   // The tensor-core path reads query rows in 16-byte pieces.
   if (d.dtype == MLA_BF16 ? !aligned(q, 16) || q_token_stride % 8 || q_head_stride % 8 : !aligned(q, 4))
     return MLA_ERR_INVALID_ARG;
+  const size_t e = esize(d);
+  const size_t q_bytes = e * ((size_t)(T - 1) * q_token_stride + (size_t)(d.n_h - 1) * q_head_stride + d.d_c + d.d_r);
+  if (overlap(q, q_bytes, out, e * (size_t)T * d.n_h * d.d_c)) return MLA_ERR_INVALID_ARG;
   const RaggedPlan P = make_ragged_plan(d, B, T);
   if (workspace_bytes < P.total) return MLA_ERR_WORKSPACE;
   g_launches = 0;

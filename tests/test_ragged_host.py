@@ -30,14 +30,19 @@ def call(fn, defaults, **kw):
 
 
 def test_plan_refusals(mla):
-    ok = dict(new_len=FAKE, past_len=FAKE, B=4, free_pages=FAKE, n_free=9, page_table=FAKE, max_pages=8, num_pages=99,
-              q_start=FAKE, kv_len=FAKE, seq_idx=FAKE, pos=FAKE, slot=FAKE, rows=5, counts=FAKE, err=None, stream=None)
+    out = FAKE + 4096
+    ok = dict(new_len=FAKE, past_len=FAKE, B=4, free_pages=FAKE, n_free=9, page_table=out, max_pages=8, num_pages=99,
+              q_start=out, kv_len=out, seq_idx=out, pos=out, slot=out, rows=5, counts=out, err=None, stream=None)
     f = mla.lib.mla_plan_step
     for bad in ("new_len", "past_len", "page_table", "q_start", "kv_len", "counts", "free_pages", "seq_idx", "pos", "slot"):
         assert call(f, ok, **{bad: None}) == INVALID, bad
         assert call(f, ok, **{bad: FAKE + 2}) == INVALID, bad
     for bad in (dict(B=0), dict(B=-1), dict(n_free=-1), dict(max_pages=0), dict(num_pages=0), dict(rows=-1),
                 dict(slot=FAKE + 4), dict(err=FAKE + 1)):
+        assert call(f, ok, **bad) == INVALID, bad
+    # Outputs in the place of lengths or free pages that other CTAs still read.
+    for bad in (dict(kv_len=FAKE), dict(q_start=FAKE + 12), dict(page_table=FAKE - 4), dict(seq_idx=FAKE + 32),
+                dict(slot=FAKE - 32), dict(counts=FAKE), dict(pos=FAKE)):
         assert call(f, ok, **bad) == INVALID, bad
     for bad in (dict(B=16385), dict(rows=2 ** 31 - 1), dict(rows=2 ** 30 + 1), dict(n_free=2 ** 31 - 1), dict(max_pages=2 ** 25)):
         assert call(f, ok, **bad) == UNSUPPORTED, bad
@@ -78,13 +83,14 @@ def test_attend_ragged_refusals_and_sizes(mla):
     d = dims(mla)
     need = mla.attend_ragged_workspace_bytes(d, 4, 70)
     assert need > 2 * 160 * 64 * 256 * 4
+    out = FAKE + 2 * 70 * 16 * 288
     ok = dict(dims=ctypes.byref(d), q=FAKE, q_ts=16 * 288, q_hs=288, q_start=FAKE, kv_len=FAKE, table=FAKE, max_pages=8,
-              num_pages=99, cache=FAKE, out=FAKE, lse=FAKE, B=4, T=70, ws=FAKE, ws_bytes=need, stream=None)
+              num_pages=99, cache=FAKE, out=out, lse=FAKE, B=4, T=70, ws=FAKE, ws_bytes=need, stream=None)
     f = mla.lib.mla_attend_ragged
     for bad in (dict(dims=None), dict(q=None), dict(q_start=None), dict(kv_len=None), dict(table=None), dict(cache=None),
                 dict(out=None), dict(ws=None), dict(B=0), dict(T=-1), dict(max_pages=0), dict(num_pages=0),
                 dict(num_pages=2 ** 26), dict(max_pages=2 ** 26), dict(q_hs=280), dict(q_ts=16 * 288 - 8),
-                dict(q_hs=289, q_ts=16 * 289), dict(q_ts=16 * 288 + 4), dict(q=FAKE + 8), dict(out=FAKE + 8),
+                dict(q_hs=289, q_ts=16 * 289), dict(q_ts=16 * 288 + 4), dict(q=FAKE + 8), dict(out=out + 8), dict(out=out - 16), dict(out=FAKE),
                 dict(ws=FAKE + 64), dict(lse=FAKE + 2)):
         assert call(f, ok, **bad) == INVALID, bad
     assert call(f, ok, ws_bytes=need - 1) == WORKSPACE
