@@ -89,36 +89,37 @@ cudaError_t launch_ragged_simt(const ragged_simt::Args& a, int W, cudaStream_t s
 // Rows per block of the normalised append: one, until the blocks fill the GPU
 // eight times over; then each walks several.
 template <typename T>
-void launch_norm_append(const step::NormAppendArgs& a, bool vec, cudaStream_t st) {
+cudaError_t launch_norm_append(const step::NormAppendArgs& a, bool vec, cudaStream_t st) {
   const int ve = vec ? 16 / (int)sizeof(T) : 1, per = a.cq ? 1 : step::NORM_THREADS / 32;
   const int grid = std::min(ceil_div(a.T, per), 8 * num_sms());
   const bool small = a.d_c <= 2 * 32 * ve && a.d_cq <= 2 * 96 * ve;  // two vectors a thread
-  if (!vec) step::norm_append_kernel<T, false, 4><<<grid, step::NORM_THREADS, 0, st>>>(a);
-  else if (small) step::norm_append_kernel<T, true, 2><<<grid, step::NORM_THREADS, 0, st>>>(a);
-  else step::norm_append_kernel<T, true, 4><<<grid, step::NORM_THREADS, 0, st>>>(a);
+  const dim3 threads(step::NORM_THREADS);
+  if (!vec) return launch_pdl(step::norm_append_kernel<T, false, 4>, dim3(grid), threads, 0, st, a);
+  if (small) return launch_pdl(step::norm_append_kernel<T, true, 2>, dim3(grid), threads, 0, st, a);
+  return launch_pdl(step::norm_append_kernel<T, true, 4>, dim3(grid), threads, 0, st, a);
 }
 
 template <typename T, bool kVec, int G, int VPL>
-void launch_query(step::QueryArgs& a, cudaStream_t st) {
+cudaError_t launch_query(step::QueryArgs& a, cudaStream_t st) {
   // Heads per block: all of a token's, unless that leaves the GPU with fewer
   // than sixteen blocks an SM; then fewer, in whole steps.
   const int step_heads = 2 * (step::QUERY_THREADS / G), steps = ceil_div(a.n_h, step_heads);
   const int want = ceil_div(16 * num_sms(), a.T), parts = std::max(1, std::min(steps, want));
   a.hpb = step_heads * ceil_div(steps, parts);
-  step::query_norm_rope_kernel<T, kVec, G, VPL>
-      <<<dim3((unsigned)a.T, (unsigned)ceil_div(a.n_h, a.hpb)), step::QUERY_THREADS, 0, st>>>(a);
+  return launch_pdl(step::query_norm_rope_kernel<T, kVec, G, VPL>, dim3((unsigned)a.T, (unsigned)ceil_div(a.n_h, a.hpb)),
+                    dim3(step::QUERY_THREADS), 0, st, a);
 }
 template <typename T>
-void launch_query(step::QueryArgs& a, bool vec, cudaStream_t st) {
+cudaError_t launch_query(step::QueryArgs& a, bool vec, cudaStream_t st) {
   const int ve = 16 / (int)sizeof(T), parts = vec ? a.d_r / ve : a.d_r / 2;  // vectors or pairs of a position part
   for (a.rope_shift = 0; (1 << a.rope_shift) < parts;) ++a.rope_shift;
   if (!vec) return launch_query<T, false, 32, 4>(a, st);
   const int nv = a.d_h / ve;
-  if (nv <= 4) launch_query<T, true, 4, 1>(a, st);
-  else if (nv <= 8) launch_query<T, true, 8, 1>(a, st);
-  else if (nv <= 16) launch_query<T, true, 16, 1>(a, st);
-  else if (nv <= 32) launch_query<T, true, 32, 1>(a, st);
-  else launch_query<T, true, 32, 4>(a, st);
+  if (nv <= 4) return launch_query<T, true, 4, 1>(a, st);
+  if (nv <= 8) return launch_query<T, true, 8, 1>(a, st);
+  if (nv <= 16) return launch_query<T, true, 16, 1>(a, st);
+  if (nv <= 32) return launch_query<T, true, 32, 1>(a, st);
+  return launch_query<T, true, 32, 4>(a, st);
 }
 
 // Schedule, attention, merge of the row blocks in pieces.  `err`: the error
@@ -284,8 +285,7 @@ mla_status mla_plan_step(const int32_t* new_len, const int32_t* past_len, int B,
   if (e) return cuda_status(e);
   g_launches = 1;
   const int ctas = std::min(num_sms(), ceil_div(std::max(rows, B + 1), step::PLAN_THREADS));
-  step::plan_kernel<<<ctas, step::PLAN_THREADS, sm, stream>>>(a);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_pdl(step::plan_kernel, dim3(ctas), dim3(step::PLAN_THREADS), sm, stream, a));
 }
 
 mla_status mla_append_normed(const mla_dims* dims, const void* kv, int64_t kv_stride, const void* kv_gamma,
@@ -321,9 +321,8 @@ mla_status mla_append_normed(const mla_dims* dims, const void* kv, int64_t kv_st
     vec = vec && aligned(cq, 16) && aligned(cq_gamma, 16) && aligned(cq_out, 16) && cq_stride % ve == 0 &&
           cq_out_stride % ve == 0 && d.d_cq % ve == 0;
   g_launches = 1;
-  if (d.dtype == MLA_BF16) launch_norm_append<__nv_bfloat16>(a, vec, stream);
-  else launch_norm_append<float>(a, vec, stream);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(d.dtype == MLA_BF16 ? launch_norm_append<__nv_bfloat16>(a, vec, stream)
+                                         : launch_norm_append<float>(a, vec, stream));
 }
 
 mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_stride, const void* gamma, float eps,
@@ -355,9 +354,8 @@ mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_st
   a.eps = eps;
   a.rope = rope_table(d);
   g_launches = 1;
-  if (d.dtype == MLA_BF16) launch_query<__nv_bfloat16>(a, vec, stream);
-  else launch_query<float>(a, vec, stream);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(d.dtype == MLA_BF16 ? launch_query<__nv_bfloat16>(a, vec, stream)
+                                         : launch_query<float>(a, vec, stream));
 }
 
 size_t mla_attend_ragged_workspace_bytes(const mla_dims* dims, int B, int T) {
