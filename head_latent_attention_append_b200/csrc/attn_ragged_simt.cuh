@@ -7,17 +7,20 @@
 //   S = Q K^T: lane (cg, kx) multiplies 8 rows with keys kx, kx + 8, kx + 16,
 //   kx + 24 over the columns 16 s + 4 cg ..; a reduce-scatter over the four
 //   column groups leaves lane `key` with the 8 rows' scores of that key;
-//   the online softmax of a row is then one warp reduction, and
+//   the online softmax takes all eight rows at once, four lanes each, by way of
+//   the warp's own rows of P, and
 //   O += P V has 8 rows x 4 NC columns (4 lane + 128 c) in a lane's registers.
 // A 16-byte shared-memory load of a warp costs four cycles whatever it shares,
 // so a tile of R x C values per lane is bound by FMAs only where R C >= 4 (R +
 // C): 8 x 4 here (4 x 2 with 256 threads, or 2 x 2 with 512, were three and
-// four times above it and took 1.5 times as long), 8 x 4 NC in P V.  A small
+// four times above it and took 1.5 times as long), 8 x 4 NC in P V.  FMAs are
+// issued in pairs, which took 4% (d_c 512) to 9% (one tile per CTA) off.  A small
 // batch is one tile per CTA and bound by latency, so all rows of a tile are
 // copied asynchronously at once, the next 32 keys while these are worked on
-// (where two buffers fit: rows of up to 432 values).  400 tokens of 16 heads over
-// up to 4000 keys run at 35 TFLOP/s; 39 tokens over up to 517 keys in 36 us, of
-// which one tile is 25.
+// (where two buffers fit: rows of up to 432 values).  One bulk copy per row
+// instead of sixteen bytes per thread: 5% faster at d_c 256 in large batches,
+// 5% slower at 512 (registers), 1% slower in small ones.  400 tokens of 16 heads
+// over up to 4000 keys run at 36 TFLOP/s; 39 tokens over up to 517 keys in 34 us.
 #pragma once
 #include "ragged_sched.cuh"
 
@@ -90,8 +93,10 @@ __device__ __forceinline__ void put_row(const Args& a, const Ctx& x, float* dst,
   }
 }
 __device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float dot4(float4 q, float4 k, float s) {
-  return fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s))));
+// Four products as two pairs (even and odd columns).
+__device__ __forceinline__ float2 dot4(float4 q, float4 k, float2 s) {
+  s = __ffma2_rn(make_float2(q.x, q.y), make_float2(k.x, k.y), s);
+  return __ffma2_rn(make_float2(q.z, q.w), make_float2(k.z, k.w), s);
 }
 
 // A segment of at most 8 MI rows.  MI is a constant so that the loops over a
@@ -121,19 +126,16 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
     put_row(a, x, x.Qs + r * P4, a.q + t * a.q_ts + (row - t * a.n_h) * a.q_hs, r < g.nrows, lane);
   }
   if (k_begin < k_end) fetch(k_begin, x.Kb);
-  int lim[MI];
-  float m[MI], l[MI], acc[MI][NC][4];
+  // The softmax state of the warp's rows: four lanes each, row lane / 4 (a warp
+  // of fewer than eight rows leaves the others at no key).
+  const int sr = lane >> 2, my_row = warp + WARPS * sr;
+  const int lim = sr < MI && my_row < g.nrows ? min(max(g.base + (g.row0 + my_row) / a.n_h + 1, 0), g.nkeys) : 0;
+  float m = -INFINITY, l = 0.f;
+  float2 acc[MI][NC][2];
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int r = warp + WARPS * i;
-    lim[i] = r < g.nrows ? min(max(g.base + (g.row0 + r) / a.n_h + 1, 0), g.nkeys) : 0;
-    m[i] = -INFINITY;
-    l[i] = 0.f;
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.f;
-  }
+    for (int c = 0; c < NC; ++c) acc[i][c][0] = acc[i][c][1] = make_float2(0.f, 0.f);
   float* const Pr = x.Ps + warp * PP;
   int buf = 0;
   for (int k0 = k_begin; k0 < k_end; k0 += KT, buf ^= a.buffers - 1) {
@@ -141,11 +143,11 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();  // this tile is there, and every thread is done with the one before
     if (a.buffers == 2 && k0 + KT < k_end) fetch(k0 + KT, x.Kb + (buf ^ 1) * KT * P4);
-    float s[MI][4];
+    float2 s2[MI][4];  // even and odd columns
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+      for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
     {
       const float* const kp = Ks + kx * P4 + 4 * cg;
       const float* const qp = x.Qs + warp * P4 + 4 * cg;
@@ -157,7 +159,7 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
         for (int i = 0; i < MI; ++i) {
           const float4 q = at4(qp + WARPS * i * P4 + c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[i][j] = dot4(q, k[j], s[i][j]);
+          for (int j = 0; j < 4; ++j) s2[i][j] = dot4(q, k[j], s2[i][j]);
         }
       }
     }
@@ -165,25 +167,52 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
     for (int i = 0; i < MI; ++i) {
       // The four column groups' sums: this lane is left with key kx + 8 cg = lane.
       const bool hi = cg & 2, odd = cg & 1;
-      const float t0 = (hi ? s[i][2] : s[i][0]) + __shfl_xor_sync(0xffffffffu, hi ? s[i][0] : s[i][2], 16);
-      const float t1 = (hi ? s[i][3] : s[i][1]) + __shfl_xor_sync(0xffffffffu, hi ? s[i][1] : s[i][3], 16);
-      const float sum4 = (odd ? t1 : t0) + __shfl_xor_sync(0xffffffffu, odd ? t0 : t1, 8);
-      const float sc = k0 + lane < lim[i] ? sum4 * a.scale : -INFINITY;
-      float mx = sc;
+      float s[4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float mn = fmaxf(m[i], mx), ref = ref_max(mn);
-      const float corr = exp2f(m[i] - ref), p = exp2f(sc - ref);
-      float sum = p;
+      for (int j = 0; j < 4; ++j) s[j] = s2[i][j].x + s2[i][j].y;
+      const float t0 = (hi ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, hi ? s[0] : s[2], 16);
+      const float t1 = (hi ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, hi ? s[1] : s[3], 16);
+      Pr[WARPS * i * PP + lane] = (odd ? t1 : t0) + __shfl_xor_sync(0xffffffffu, odd ? t0 : t1, 8);
+    }
+    __syncwarp();
+    {
+      // All rows at once: lane holds eight keys of row sr.
+      float* const pr = Pr + WARPS * min(sr, MI - 1) * PP + 8 * (lane & 3);
+      const float4 xa = at4(pr), xb = at4(pr + 4);
+      float x[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+      const int seen = lim - k0 - 8 * (lane & 3);  // of these eight
+      float mx = -INFINITY;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l[i] = fmaf(l[i], corr, sum);
-      m[i] = mn;
-      Pr[WARPS * i * PP + lane] = p;
+      for (int e = 0; e < 8; ++e) {
+        x[e] = e < seen ? x[e] * a.scale : -INFINITY;
+        mx = fmaxf(mx, x[e]);
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m, mx), ref = ref_max(mn), corr = exp2f(m - ref);
+      float sum = 0.f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+      for (int e = 0; e < 8; ++e) {
+        x[e] = exp2f(x[e] - ref);
+        sum += x[e];
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      l = fmaf(l, corr, sum);
+      m = mn;
+      __syncwarp();  // lanes of a row that does not exist read another's scores
+      if (sr < MI) {
+        *reinterpret_cast<float4*>(pr) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(pr + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][c][e] *= corr;
+      for (int i = 0; i < MI; ++i) {
+        const float ci = __shfl_sync(0xffffffffu, corr, 4 * i);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) acc[i][c][e] = __fmul2_rn(acc[i][c][e], make_float2(ci, ci));
+      }
     }
     __syncwarp();
     if (k0 + KT > g.kmin) {
@@ -210,10 +239,8 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
 #pragma unroll
           for (int i = 0; i < MI; ++i) {
             const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-            acc[i][c][0] = fmaf(w, v.x, acc[i][c][0]);
-            acc[i][c][1] = fmaf(w, v.y, acc[i][c][1]);
-            acc[i][c][2] = fmaf(w, v.z, acc[i][c][2]);
-            acc[i][c][3] = fmaf(w, v.w, acc[i][c][3]);
+            acc[i][c][0] = __ffma2_rn(make_float2(w, w), make_float2(v.x, v.y), acc[i][c][0]);
+            acc[i][c][1] = __ffma2_rn(make_float2(w, w), make_float2(v.z, v.w), acc[i][c][1]);
           }
         }
     }
@@ -231,21 +258,22 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
                                          : a.o.part_o + (long long)g.slot * ROWS * x.dcp)
                            : x.Qs;
   const int step = wide ? x.dcp : P4;
+  if ((lane & 3) == 0 && sr < MI && my_row < g.nrows) {
+    if (g.slot >= 0) a.o.part_ml[(long long)g.slot * ROWS + my_row] = make_float2(m, l);
+    else if (a.o.lse) a.o.lse[(long long)g.row0 + my_row] = row_lse(ref_max(m), l);
+  }
+  const float row_factor = row_inv(l);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int r = warp + WARPS * i;
+    const float inv = __shfl_sync(0xffffffffu, row_factor, 4 * i);
     if (r >= g.nrows) continue;
-    const float inv = row_inv(l[i]);
     float* const dst = base + r * step + 4 * lane;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
       if (4 * lane + 128 * c < x.dcp)
         *reinterpret_cast<float4*>(dst + 128 * c) =
-            make_float4(acc[i][c][0] * inv, acc[i][c][1] * inv, acc[i][c][2] * inv, acc[i][c][3] * inv);
-    if (lane == 0) {
-      if (g.slot >= 0) a.o.part_ml[(long long)g.slot * ROWS + r] = make_float2(m[i], l[i]);
-      else if (a.o.lse) a.o.lse[(long long)g.row0 + r] = row_lse(ref_max(m[i]), l[i]);
-    }
+            make_float4(acc[i][c][0].x * inv, acc[i][c][0].y * inv, acc[i][c][1].x * inv, acc[i][c][1].y * inv);
   }
   if (!wide) {
     __syncwarp();
