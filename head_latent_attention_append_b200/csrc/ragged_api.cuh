@@ -139,11 +139,12 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
   cudaError_t e;
   {
     const int ints = (int)std::min<long long>(B + 1 + 3LL * (P.r_max + 1), kRaggedSmemInts);
-    const RaggedSchedArgs a{q_start, kv_len, B, T, d.n_h, P.rows, W, max_pages, P.r_max,
+    const RaggedSchedArgs a{q_start, kv_len, B, T, d.n_h, P.rows, W, max_pages,
                             block_tiles(d), keep_err, S, err, ints};
     if ((e = set_smem_once(ragged_sched_kernel, sizeof(int) * (size_t)kRaggedSmemInts))) return cuda_status(e);
     ++g_launches;
-    if ((e = launch_pdl(ragged_sched_kernel, dim3(1), dim3(P.r_max <= 256 ? 256 : P.r_max <= kSchedSmall ? kSchedSmall : 1024), sizeof(int) * (size_t)ints, st, a)))
+    const int threads = P.r_max <= 256 ? 256 : P.r_max <= kSchedSmall ? kSchedSmall : 1024;
+    if ((e = launch_pdl(ragged_sched_kernel, dim3(1), dim3(threads), sizeof(int) * (size_t)ints, st, a)))
       return cuda_status(e);
   }
   ++g_launches;

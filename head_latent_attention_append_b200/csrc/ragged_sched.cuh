@@ -50,7 +50,7 @@ __host__ __device__ __forceinline__ int ragged_slot(int w0, int k) { return k > 
 struct RaggedSchedArgs {
   const int32_t* q_start;  // [B+1]
   const int32_t* kv_len;   // [B]
-  int B, T, n_h, rows, W, max_pages, r_max, block_tiles;
+  int B, T, n_h, rows, W, max_pages, block_tiles;
   int keep_err;            // the error word is an earlier launch's too: do not zero it
   RaggedSched s;
   int* err;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   if (small) {
     long long sum;
     const int n_blocks = tid < a.B ? bs[tid] : 0, first_rb = block_scan_once(n_blocks, words[0], &sum);
-    const int R = (int)sum;  // <= r_max: the starts are in order
+    const int R = (int)sum;
     if (R <= nt) {
       if (tid < a.B) bs[tid] = first_rb;
       __syncthreads();
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   }
 
   int* const off = rs_smem;
-  const int R = (int)ragged_scan(off, a.B);  // <= r_max
+  const int R = (int)ragged_scan(off, a.B);  // at most what the workspace holds: the starts are in order
   if (tid == 0) off[a.B] = R;
   const bool in_smem = a.B + 1 + 3 * (R + 1) <= a.smem_ints;
   int* const vs = in_smem ? off + a.B + 1 : a.s.vs;
