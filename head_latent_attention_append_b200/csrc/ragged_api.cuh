@@ -300,6 +300,7 @@ mla_status mla_append_normed(const mla_dims* dims, const void* kv, int64_t kv_st
   if (T < 0 || num_pages <= 0 || !(eps >= 0.f) || kv_stride < d_cr) return MLA_ERR_INVALID_ARG;
   if ((cq != nullptr) != (cq_out != nullptr) || (!cq && cq_gamma)) return MLA_ERR_INVALID_ARG;
   if (cq && (d.d_cq <= 0 || cq_stride < d.d_cq || cq_out_stride < d.d_cq)) return MLA_ERR_INVALID_ARG;
+  if (T > (1 << 30)) return MLA_ERR_UNSUPPORTED;  // a warp's next row in 32 bits
   if (T == 0) return MLA_OK;
   if (!kv || !pos || !slot || !cache) return MLA_ERR_INVALID_ARG;
   const size_t e = esize(d);

@@ -343,7 +343,8 @@ mla_status mla_prefill_materialised(const mla_weights* w, const void* h, const i
  * A request with a negative length, or one longer than max_pages*64, counts as
  * empty with kv_len 0; a page id outside [0, num_pages) gives slot -1; both OR
  * 1 into *device_error (device int32, NULL to ignore, zeroed by the caller).
- * B <= 16384, else MLA_ERR_UNSUPPORTED.  Needs no workspace. */
+ * B <= 16384, rows and n_free <= 2^30, else MLA_ERR_UNSUPPORTED.  Needs no
+ * workspace. */
 mla_status mla_plan_step(const int32_t* new_len, const int32_t* past_len, int B,
                          const int32_t* free_pages, int n_free, int32_t* page_table, int max_pages,
                          int num_pages, int32_t* q_start, int32_t* kv_len, int32_t* seq_idx,
@@ -360,7 +361,8 @@ mla_status mla_plan_step(const int32_t* new_len, const int32_t* past_len, int B,
  * taken in 32 bits (angles in 64) and rounded once.  slot -1 leaves the cache
  * alone; any other slot outside [0, num_pages*64) does too and ORs 1 into
  * *device_error (may be NULL).  Slots other than -1 must differ.  Rows that
- * start on 16-byte boundaries are moved fastest; any element alignment works. */
+ * start on 16-byte boundaries are moved fastest; any element alignment works.
+ * T <= 2^30, else MLA_ERR_UNSUPPORTED. */
 mla_status mla_append_normed(const mla_dims* dims, const void* kv, int64_t kv_stride,
                              const void* kv_gamma, const void* cq, int64_t cq_stride,
                              const void* cq_gamma, void* cq_out, int64_t cq_out_stride, float eps,
@@ -394,9 +396,12 @@ mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_st
  * they are.  Cache rows that no query sees may hold anything.  q_start that
  * decreases or leaves [0, T] computes nothing; a length outside
  * [0, max_pages*64] counts as the nearest one, and the outputs of a request with
- * a page id outside [0, num_pages) are unspecified; each sets
- * MLA_ERR_DEVICE_BOUNDS in the workspace error word.  A NaN or infinity in a key
- * that a query does not see does not reach it.  Deterministic.  One shared RoPE key and B <= 16384 (else
+ * a page id outside [0, num_pages) are unspecified; a batch of more than 2^31 - 1
+ * (128 rows x 64 keys) tiles computes nothing; each sets MLA_ERR_DEVICE_BOUNDS
+ * in the workspace error word.  A NaN or infinity in a key that a query does not
+ * see does not reach it; one that it does see makes its row NaN, but for an
+ * infinity that brings the key's score to -inf, which may count as weight 0.
+ * Deterministic.  One shared RoPE key, B <= 16384 and T * n_h < 2^31 - 128 (else
  * MLA_ERR_UNSUPPORTED).  Workspace: mla_attend_ragged_workspace_bytes, for at
  * least this B and T. */
 size_t mla_attend_ragged_workspace_bytes(const mla_dims* dims, int B, int T);

@@ -106,6 +106,18 @@ def test_attend_ragged_refusals_and_sizes(mla):
     assert sizes == sorted(sizes)
 
 
+def test_rows_past_32_bits_are_refused(mla):
+    """A warp of the normalised append counts on from its row by a whole grid: T leaves room for that."""
+    f = mla.lib.mla_append_normed
+    for d in (dims(mla), dims(mla, dtype=mla.F32), dims(mla, dtype=mla.F32, d_c=16, d_r=2)):
+        ok = dict(dims=ctypes.byref(d), kv=FAKE, kv_stride=288, kv_gamma=None, cq=None, cq_stride=0, cq_gamma=None,
+                  cq_out=None, cq_out_stride=0, eps=1e-6, pos=FAKE, slot=FAKE, cache=FAKE, num_pages=4, T=0, err=None,
+                  stream=None)
+        assert call(f, ok) == 0
+        for T in (2 ** 31 - 1, 2 ** 30 + 1):
+            assert call(f, ok, T=T) == UNSUPPORTED
+
+
 def test_the_binding_refuses_tensors_it_could_not_pass_on(mla):
     """Shapes, types and devices are checked before the library sees an address; tensors on the CPU never get there."""
     d = dims(mla, d_cq=0)
