@@ -17,7 +17,8 @@
 //     last key (at most 1 + 128 / n_h / 64 of a row block) need a mask, and in those the latent
 //     rows are cleared of what a weight of 0 must not meet: rows behind the
 //     block's last key wholly, infinities and NaNs in rows that only some of
-//     the block's rows see (a row that sees one has a NaN sum already);
+//     the block's rows see (a row that sees one has a NaN sum already, or a
+//     score of -inf there and with it no weight);
 //   - the softmax scale is applied to the scores in 32 bits (one FMA with the
 //     running maximum), so the queries come as they are;
 //   - a piece of a cut row block leaves its O in 32 bits, column by column, so

@@ -217,7 +217,8 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
     __syncwarp();
     if (k0 + KT > g.kmin) {
       // Keys that only some of the rows see: a weight of 0 must not meet an
-      // infinity or a NaN.  A row that does see one already has a NaN sum.
+      // infinity or a NaN.  A row that does see one already has a NaN sum, or a
+      // score of -inf there and with it no weight.
       __syncthreads();
       for (int r = max(0, g.kmin - k0) + warp; r < KT; r += WARPS)
         for (int c = lane; c < x.dcp; c += 32)

@@ -202,52 +202,47 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   if (small) {
     long long sum;
     const int n_blocks = tid < a.B ? bs[tid] : 0, first_rb = block_scan_once(n_blocks, words[0], &sum);
-    const int R = (int)sum;
-    if (R <= nt) {
-      if (tid < a.B) bs[tid] = first_rb;
-      __syncthreads();
-      const bool mine = tid < R;
-      RSeg g{};
-      int v = 0;
-      if (mine) {
-        const int b = find_le(bs, a.B, tid);
-        const int4 q = req[b];
-        g = ragged_block(a, b, tid - bs[b], q.x, q.y, q.z);
-        v = ragged_tiles(g) + a.block_tiles;
-        blocks[tid] = g;
-      }
-      const int v0 = block_scan_once(v, words[1], &sum);
-      if (R == 0 || sum > 0x7fffffffLL) {
-        if (tid == 0 && R > 0) flag_error(a.err, kErrBounds);
-        for (int w = tid; w <= a.W; w += nt) a.s.worker_seg[w] = 0;
-        return;
-      }
-      const RaggedShares sh((int)sum, a.W, a.block_tiles);
-      int pieces = 0;
-      if (mine) {
-        const int w0 = sh.owner(v0 + a.block_tiles);
-        pieces = sh.owner(v0 + v - 1) - w0 + 1;
-        wf_s[tid] = w0;
-        vs_s[tid] = v0;
-      }
-      const int s0 = block_scan_once(pieces, words[2], &sum);
-      if (mine) pc_s[tid] = s0;
-      const int nseg = (int)sum;
-      if (tid == 0) {
-        pc_s[R] = nseg;
-        vs_s[R] = sh.total;
-      }
-      __syncthreads();
-      for (int s = tid; s < nseg; s += nt) {
-        const int rb = find_le(pc_s, R, s), k = s - pc_s[rb], w = wf_s[rb] + k;
-        const int before = k > 0 ? w - 1 : (rb > 0 ? wf_s[rb - 1] + s - pc_s[rb - 1] - 1 : -1);
-        sh.emit(a, blocks[rb], s, k, pc_s[rb + 1] - pc_s[rb], vs_s[rb], vs_s[rb + 1], w, before, s == nseg - 1);
-      }
+    const int R = (int)sum;  // at most the workspace's row blocks, for which there are threads
+    if (tid < a.B) bs[tid] = first_rb;
+    __syncthreads();
+    const bool mine = tid < R;
+    RSeg g{};
+    int v = 0;
+    if (mine) {
+      const int b = find_le(bs, a.B, tid);
+      const int4 q = req[b];
+      g = ragged_block(a, b, tid - bs[b], q.x, q.y, q.z);
+      v = ragged_tiles(g) + a.block_tiles;
+      blocks[tid] = g;
+    }
+    const int v0 = block_scan_once(v, words[1], &sum);
+    if (R == 0 || sum > 0x7fffffffLL) {
+      if (tid == 0 && R > 0) flag_error(a.err, kErrBounds);
+      for (int w = tid; w <= a.W; w += nt) a.s.worker_seg[w] = 0;
       return;
     }
-    // Many row blocks of few requests: the offsets go where the long way has them.
-    for (int b = tid; b < a.B; b += nt) rs_smem[b] = bs_s[b];
+    const RaggedShares sh((int)sum, a.W, a.block_tiles);
+    int pieces = 0;
+    if (mine) {
+      const int w0 = sh.owner(v0 + a.block_tiles);
+      pieces = sh.owner(v0 + v - 1) - w0 + 1;
+      wf_s[tid] = w0;
+      vs_s[tid] = v0;
+    }
+    const int s0 = block_scan_once(pieces, words[2], &sum);
+    if (mine) pc_s[tid] = s0;
+    const int nseg = (int)sum;
+    if (tid == 0) {
+      pc_s[R] = nseg;
+      vs_s[R] = sh.total;
+    }
     __syncthreads();
+    for (int s = tid; s < nseg; s += nt) {
+      const int rb = find_le(pc_s, R, s), k = s - pc_s[rb], w = wf_s[rb] + k;
+      const int before = k > 0 ? w - 1 : (rb > 0 ? wf_s[rb - 1] + s - pc_s[rb - 1] - 1 : -1);
+      sh.emit(a, blocks[rb], s, k, pc_s[rb + 1] - pc_s[rb], vs_s[rb], vs_s[rb + 1], w, before, s == nseg - 1);
+    }
+    return;
   }
 
   int* const off = rs_smem;
