@@ -77,6 +77,8 @@ using attn_tc::VGS;
 
 constexpr int ROWS = 128;          // rows of a row block
 constexpr int CROWS = ROWS / 2;    // rows per CTA
+constexpr int kOwnMost = THREADS;  // requests and row blocks of a schedule that every CTA makes for itself
+static_assert(sizeof(RaggedScratch<kOwnMost>) <= VGS * VG_BYTES, "the schedule's sums fit the latent ring");
 
 struct Args {
   const __nv_bfloat16* q;      // row r of token t, head h: q + t * q_ts + h * q_hs, d_c + d_r values
@@ -85,9 +87,8 @@ struct Args {
   int max_pages, num_pages, n_h, d_c, q_row;
   float scale;                 // softmax scale times log2 e
   int q_dense;                 // the rows of q are contiguous
-  RaggedSched sched;
+  RaggedSchedArgs sched;
   RaggedOut o;
-  int* err;
 };
 
 // Walks a worker's segments page by page, the next page's id loaded one step
@@ -142,7 +143,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   static_assert(NPV >= 1 && NPV <= MAX_NPV && NSS * CH_V <= QS_BYTES, "latent width");
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the same in every CTA: all leave before any barrier
-    if (threadIdx.x == 0) flag_error(a.err, kErrLayout);
+    if (threadIdx.x == 0) a.sched.s.worker_err[blockIdx.x] = kErrLayout;
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
@@ -159,6 +160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint64_t* final_bar = o_free + 1;        // the MMA issuer's last commit
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  int* const err = reinterpret_cast<int*>(smem + OFF_MISC + 8);  // this CTA's error bits
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
@@ -183,6 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mbar_init(o_free, 16);
     mbar_init(final_bar, 1);
     *abort_flag = 0;
+    *err = 0;
     mbar_fence_init();
   }
   if (warp == 2) {
@@ -197,11 +200,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync_all();  // the peer's barriers and TMEM exist before anyone signals them
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  // Everything above overlaps the schedule kernel.
+  // Everything above overlaps the kernel before this one.
   pdl_wait();
   pdl_trigger();
-  const RSeg* segs = a.sched.segs;
-  const int seg_lo = a.sched.worker_seg[w], seg_hi = a.sched.worker_seg[w + 1];
+  const RSeg* segs = a.sched.s.segs;
+  int2* const range = a.sched.s.range + (a.sched.own ? blockIdx.x : w);
+  if (a.sched.own) {
+    ragged_schedule<kOwnMost>(a.sched, *reinterpret_cast<RaggedScratch<kOwnMost>*>(smem + OFF_VG), w, range, err);
+    fence_proxy_async_smem();  // the latent ring's copies land where the sums were
+    __syncthreads();
+  }
+  const int seg_lo = range->x, seg_hi = range->y;
 
   if (warp == 0 || warp == 2) {
     // ---------------------------------------------------- TMA producers
@@ -217,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int slot_bytes = score_ring ? SG_BYTES : VG_BYTES;
     const uint32_t full_even = map_peer(smem_u32(full), 0);
     PageWalk pw{segs, a.page_table, a.max_pages, 0, seg_hi, 0, RSeg{}, RSeg{}, false, 0};
-    pw.start(seg_lo, a.sched.first[w]);
+    pw.start(seg_lo, a.sched.s.first[w]);
     static_assert(VGS == 2, "two latent slots");
     uint32_t cnt = 0, part_cnt0 = 0, part_cnt1 = 0;  // edge loads per latent slot
     while (pw.more) {
@@ -225,10 +234,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int t;
       int page = pw.next(g, t);
       const uint32_t s = cnt % nslots;
-      if (!mbar_wait_warp(&empty[s], ((cnt / nslots) & 1) ^ 1, abort_flag, a.err)) break;
+      if (!mbar_wait_warp(&empty[s], ((cnt / nslots) & 1) ^ 1, abort_flag, err)) break;
       if (page < 0 || page >= a.num_pages) {
         // A block that sees no key walks one page all the same, masked whole.
-        if (g.nkeys > 0 && rank == 0 && score_ring && elect_one()) flag_error(a.err, kErrBounds);
+        if (g.nkeys > 0 && rank == 0 && score_ring && elect_one()) flag_error(err, kErrBounds);
         page = 0;
       }
       const bool edge = edge_page(g, t);
@@ -284,9 +293,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // for both CTAs to have read the previous segment's O).
     auto issue_pv = [&](uint32_t pj, bool first, uint32_t sk) -> bool {
       const uint32_t vs = pj % VGS;
-      bool r_ok = mbar_wait(&vg_full[vs], (pj / VGS) & 1, abort_flag, a.err);
-      if (r_ok && first && sk > 0) r_ok = mbar_wait(o_free, (sk - 1) & 1, abort_flag, a.err);
-      if (r_ok) r_ok = mbar_wait(&p_ready[pj & 1], (pj >> 1) & 1, abort_flag, a.err);
+      bool r_ok = mbar_wait(&vg_full[vs], (pj / VGS) & 1, abort_flag, err);
+      if (r_ok && first && sk > 0) r_ok = mbar_wait(o_free, (sk - 1) & 1, abort_flag, err);
+      if (r_ok) r_ok = mbar_wait(&p_ready[pj & 1], (pj >> 1) & 1, abort_flag, err);
       if (!__all_sync(0xffffffffu, r_ok)) return false;
       tc_fence_after();
       if (elect_one()) {
@@ -314,10 +323,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           // The previous segment's last P*V first, then this segment's Q.
           if (have_prev && !(ok = issue_pv(prev_j, prev_first, prev_sk))) break;
           have_prev = false;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_ready, seg_k & 1, abort_flag, a.err)))) break;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_ready, seg_k & 1, abort_flag, err)))) break;
         }
         const uint32_t gs = j % SGS;
-        if (!(ok = mbar_wait_warp(&sg_full[gs], (j / SGS) & 1, abort_flag, a.err))) break;
+        if (!(ok = mbar_wait_warp(&sg_full[gs], (j / SGS) & 1, abort_flag, err))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t d = tS + (j & 1) * 32;
@@ -368,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // that the named barriers always see all of their threads.
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-      bool r_ok = mbar_wait(bar, parity, abort_flag, a.err);
+      bool r_ok = mbar_wait(bar, parity, abort_flag, err);
       return __all_sync(0xffffffffu, r_ok);
     };
     auto signal_even = [&](uint32_t bar_even) {
@@ -448,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // its ends (three segments in registers were 4% slower, a ring of them in
     // shared memory 2%).
     if (seg_lo < seg_hi) {  // every softmax thread: q_store holds named barriers
-      q_issue(a.sched.first[w]);
+      q_issue(a.sched.s.first[w]);
       q_store();
     }
     for (int si = seg_lo; si < seg_hi; ++si) {
@@ -678,6 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // no CTA leaves while its peer may still use its shared memory or TMEM
+  if (tid == 0) a.sched.s.worker_err[blockIdx.x] = *err;
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tbase, TM_COLS);

@@ -20,7 +20,7 @@
 // (where two buffers fit: rows of up to 432 values).  One bulk copy per row
 // instead of sixteen bytes per thread: 5% faster at d_c 256 in large batches,
 // 5% slower at 512 (registers), 1% slower in small ones.  400 tokens of 16 heads
-// over up to 4000 keys run at 36 TFLOP/s; 39 tokens over up to 517 keys in 34 us.
+// over up to 4000 keys run at 36 TFLOP/s; 39 tokens over up to 517 keys in 32 us.
 #pragma once
 #include "ragged_sched.cuh"
 
@@ -36,9 +36,12 @@ __host__ __device__ constexpr int pad4(int n) { return (n + 3) & ~3; }
 __host__ __device__ constexpr int row_cols(int d_c, int d_r) { return (pad4(d_c) + pad4(d_r) + 15) & ~15; }
 __host__ __device__ constexpr int pitch(int d_c, int d_r) { return row_cols(d_c, d_r) + 4; }
 inline size_t smem_bytes(int d_c, int d_r, int buffers) {
-  return sizeof(float) * ((size_t)(ROWS + buffers * KT) * pitch(d_c, d_r) + ROWS * PP);
+  return sizeof(float) * ((size_t)(ROWS + buffers * KT) * pitch(d_c, d_r) + ROWS * PP) + 16;  // the last 16: the error word
 }
 constexpr size_t MAX_SMEM = 232448;
+constexpr int kOwnMost = THREADS;  // requests and row blocks of a schedule that every CTA makes for itself
+static_assert(sizeof(RaggedScratch<kOwnMost>) <= sizeof(float) * ((ROWS + KT) * 20 + ROWS * PP),
+              "the schedule's sums fit the smallest rows' tiles");
 inline int key_buffers(int d_c, int d_r) { return smem_bytes(d_c, d_r, 2) <= MAX_SMEM ? 2 : 1; }
 
 // 16 bytes from global to shared memory without passing through registers, or
@@ -56,14 +59,14 @@ struct Args {
   int max_pages, num_pages, n_h, d_c, d_r;
   int buffers;               // key tiles in shared memory, 1 or 2
   float scale;               // softmax scale times log2 e
-  RaggedSched sched;
+  RaggedSchedArgs sched;
   RaggedOut o;
-  int* err;
 };
 
 // Where a segment's rows and keys are.
 struct Ctx {
   float *Qs, *Kb, *Ps;  // [ROWS][P4], [buffers][KT][P4], [ROWS][PP]
+  int* err;             // this CTA's error bits
   int d_cr, dcp, wq, P4;
   bool vec;
 };
@@ -112,7 +115,7 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
   auto fetch = [&](int k0, float* dst) {
     const int page = page_next;
     const bool ok = page >= 0 && page < a.num_pages;
-    if (!ok && tid == 0) flag_error(a.err, kErrBounds);
+    if (!ok && tid == 0) flag_error(x.err, kErrBounds);
     const float* const src = a.cache + ((long long)(ok ? page : 0) * 64 + k0 % 64) * x.d_cr;
 #pragma unroll 1
     for (int r = warp; r < KT; r += WARPS)
@@ -287,7 +290,7 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
 
 template <int NC>
 __global__ void __launch_bounds__(THREADS, 1) attn_ragged_simt_kernel(const __grid_constant__ Args a) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   Ctx x;
   x.d_cr = a.d_c + a.d_r;
   x.dcp = pad4(a.d_c);
@@ -300,15 +303,25 @@ __global__ void __launch_bounds__(THREADS, 1) attn_ragged_simt_kernel(const __gr
           ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.cache)) & 15) == 0;
   sm100::pdl_wait();
   sm100::pdl_trigger();
-  const int seg_lo = a.sched.worker_seg[blockIdx.x], seg_hi = a.sched.worker_seg[blockIdx.x + 1];
-  RSeg g = a.sched.first[blockIdx.x];
+  x.err = reinterpret_cast<int*>(x.Ps + ROWS * PP);
+  if (threadIdx.x == 0) *x.err = 0;
+  __syncthreads();
+  int2* const range = a.sched.s.range + blockIdx.x;
+  if (a.sched.own) {
+    ragged_schedule<kOwnMost>(a.sched, *reinterpret_cast<RaggedScratch<kOwnMost>*>(sm), blockIdx.x, range, x.err);
+    __syncthreads();
+  }
+  const int seg_lo = range->x, seg_hi = range->y;
+  RSeg g = a.sched.s.first[blockIdx.x];
   for (int si = seg_lo; si < seg_hi; ++si) {
-    if (si > seg_lo) g = a.sched.segs[si];
+    if (si > seg_lo) g = a.sched.s.segs[si];
     if (g.nrows <= 8) run_segment<NC, 1>(a, x, g);
     else if (g.nrows <= 16) run_segment<NC, 2>(a, x, g);
     else if (g.nrows <= 32) run_segment<NC, 4>(a, x, g);
     else run_segment<NC, 8>(a, x, g);
   }
+  __syncthreads();
+  if (threadIdx.x == 0) a.sched.s.worker_err[blockIdx.x] = *x.err;
 }
 
 }  // namespace ragged_simt

@@ -15,7 +15,7 @@ constexpr int kRaggedPairs = 80, kRaggedCtas = 160;
 int block_tiles(const mla_dims& d) { return d.dtype == MLA_BF16 ? 3 + 3 * d.d_c / 256 : 1; }
 
 struct RaggedPlan {
-  size_t hdr, vs, pc, wf, worker_seg, segs, first, split, part_o, part_ml, total;
+  size_t hdr, vs, pc, wf, range, segs, first, split, worker_err, part_o, part_ml, total;
   int rows, cap, r_max;
 };
 RaggedPlan make_ragged_plan(const mla_dims& d, int B, int T) {
@@ -28,10 +28,11 @@ RaggedPlan make_ragged_plan(const mla_dims& d, int B, int T) {
   P.vs = o;         o = align_up(o + sizeof(int) * ((size_t)P.r_max + 1), 256);
   P.pc = o;         o = align_up(o + sizeof(int) * ((size_t)P.r_max + 1), 256);
   P.wf = o;         o = align_up(o + sizeof(int) * ((size_t)P.r_max + 1), 256);
-  P.worker_seg = o; o = align_up(o + sizeof(int) * ((size_t)P.cap + 1), 256);
+  P.range = o;      o = align_up(o + sizeof(int2) * 2 * (size_t)P.cap, 256);
   P.segs = o;       o = align_up(o + sizeof(RSeg) * ((size_t)P.cap + P.r_max), 256);
   P.first = o;      o = align_up(o + sizeof(RSeg) * (size_t)P.cap, 256);
   P.split = o;      o = align_up(o + sizeof(int4) * (size_t)P.cap, 256);
+  P.worker_err = o; o = align_up(o + sizeof(int) * 2 * (size_t)P.cap, 256);
   P.part_o = o;     o = align_up(o + sizeof(float) * 2 * P.cap * P.rows * (size_t)align_up(d.d_c, 4), 256);
   P.part_ml = o;    o = align_up(o + sizeof(float2) * 2 * P.cap * P.rows, 256);
   P.total = o;
@@ -122,9 +123,10 @@ cudaError_t launch_query(step::QueryArgs& a, bool vec, cudaStream_t st) {
   return launch_query<T, true, 32, 4>(a, st);
 }
 
-// Schedule, attention, merge of the row blocks in pieces.  `err`: the error
-// word, zeroed by the schedule unless an earlier launch of the call reports
-// there too.
+// Schedule (in the attention kernel, where the batch is small enough),
+// attention, merge of the row blocks in pieces.  `err`: the error word, zeroed
+// or written by the first launch here that reports, unless an earlier one of the
+// call reports there too.
 mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, long long q_hs, const int32_t* q_start,
                               const int32_t* kv_len, const int32_t* page_table, int B, int T, int max_pages,
                               int num_pages, const void* cache, void* out, float* lse, void* ws, const RaggedPlan& P,
@@ -133,25 +135,28 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
   const int W = std::max(1, std::min(P.cap, tc ? num_sms() / 2 : num_sms()));
   const float scale =
       (float)((d.softmax_scale > 0.f ? (double)d.softmax_scale : 1.0 / sqrt((double)(d.d_h + d.d_r))) * kLog2e);
-  const RaggedSched S{at<int>(ws, P.vs), at<int>(ws, P.pc), at<int>(ws, P.wf), at<int>(ws, P.worker_seg),
-                      at<RSeg>(ws, P.segs), at<RSeg>(ws, P.first), at<int>(ws, P.hdr) + 1, at<int4>(ws, P.split)};
+  const RaggedSched S{at<int>(ws, P.vs), at<int>(ws, P.pc), at<int>(ws, P.wf), at<int2>(ws, P.range),
+                      at<RSeg>(ws, P.segs), at<RSeg>(ws, P.first), at<int4>(ws, P.split), at<int>(ws, P.worker_err)};
   const RaggedOut o{out, lse, at<float>(ws, P.part_o), at<float2>(ws, P.part_ml), d.d_c};
   cudaError_t e;
-  {
-    const int ints = (int)std::min<long long>(B + 1 + 3LL * (P.r_max + 1), kRaggedSmemInts);
-    const RaggedSchedArgs a{q_start, kv_len, B, T, d.n_h, P.rows, W, max_pages,
-                            block_tiles(d), keep_err, S, err, ints};
+  // Who makes the schedule (ragged_schedule).
+  const bool own = std::max(B, P.r_max) <= (tc ? ragged_tc::kOwnMost : ragged_simt::kOwnMost);
+  const bool one_go = std::max(B, P.r_max) <= kOneGoMost;
+  const int ints = one_go ? (int)(sizeof(RaggedScratch<kOneGoMost>) / sizeof(int))
+                          : (int)std::min<long long>(B + 1 + 3LL * (P.r_max + 1), kRaggedSmemInts);
+  const RaggedSchedArgs sa{q_start, kv_len, B, T, d.n_h, P.rows, W, max_pages, block_tiles(d), keep_err, S, err, own,
+                           one_go, ints};
+  if (!own) {
     if ((e = set_smem_once(ragged_sched_kernel, sizeof(int) * (size_t)kRaggedSmemInts))) return cuda_status(e);
     ++g_launches;
-    const int threads = P.r_max <= 256 ? 256 : P.r_max <= kSchedSmall ? kSchedSmall : 1024;
-    if ((e = launch_pdl(ragged_sched_kernel, dim3(1), dim3(threads), sizeof(int) * (size_t)ints, st, a)))
+    if ((e = launch_pdl(ragged_sched_kernel, dim3(1), dim3(1024), sizeof(int) * (size_t)ints, st, sa)))
       return cuda_status(e);
   }
   ++g_launches;
   prof_mark(st, true);
   if (tc) {
     ragged_tc::Args a{static_cast<const __nv_bfloat16*>(q), q_ts, q_hs, page_table, max_pages, num_pages, d.n_h, d.d_c,
-                      d.d_c + d.d_r, scale, q_hs == d.d_c + d.d_r && q_ts == d.n_h * q_hs, S, o, err};
+                      d.d_c + d.d_r, scale, q_hs == d.d_c + d.d_r && q_ts == d.n_h * q_hs, sa, o};
     // Score ring: 32-row boxes (one CTA's keys of a page); latent ring: 64-row boxes.
     CUtensorMap mapS, mapV;
     const long long rows = (long long)num_pages * d.page_size;
@@ -165,7 +170,7 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
     }
   } else {
     ragged_simt::Args a{static_cast<const float*>(q), q_ts, q_hs, static_cast<const float*>(cache), page_table,
-                        max_pages, num_pages, d.n_h, d.d_c, d.d_r, ragged_simt::key_buffers(d.d_c, d.d_r), scale, S, o, err};
+                        max_pages, num_pages, d.n_h, d.d_c, d.d_r, ragged_simt::key_buffers(d.d_c, d.d_r), scale, sa, o};
     if (d.d_c <= 128) e = launch_ragged_simt<1>(a, W, st);
     else if (d.d_c <= 256) e = launch_ragged_simt<2>(a, W, st);
     else e = launch_ragged_simt<4>(a, W, st);
@@ -174,8 +179,13 @@ mla_status attend_ragged_impl(const mla_dims& d, const void* q, long long q_ts, 
   prof_mark(st, false);
   ++g_launches;
   const dim3 grid(W, ceil_div(d.d_c, kCombineCols));
-  if (tc) e = launch_pdl(ragged_combine_kernel<__nv_bfloat16, ragged_tc::ROWS, true>, grid, dim3(kCombineThreads), 0, st, S, o);
-  else e = launch_pdl(ragged_combine_kernel<float, ragged_simt::ROWS, false>, grid, dim3(kCombineThreads), 0, st, S, o);
+  const int err_ctas = tc ? 2 * W : W, keep = keep_err || !own;  // the schedule kernel leaves bits there too
+  if (tc)
+    e = launch_pdl(ragged_combine_kernel<__nv_bfloat16, ragged_tc::ROWS, true>, grid, dim3(kCombineThreads), 0, st, S, o,
+                   err_ctas, err, keep);
+  else
+    e = launch_pdl(ragged_combine_kernel<float, ragged_simt::ROWS, false>, grid, dim3(kCombineThreads), 0, st, S, o,
+                   err_ctas, err, keep);
   return cuda_status(e);
 }
 

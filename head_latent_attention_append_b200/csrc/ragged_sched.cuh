@@ -36,11 +36,12 @@ struct RaggedSched {
   int* vs;          // [R+1] first (weighted) tile of each row block
   int* pc;          // [R+1] first segment of each row block
   int* wf;          // [R]   worker of that segment
-  int* worker_seg;  // [W+1] first segment of each worker
+  int2* range;      // [W] each worker's segments, [x, y); CTAs that make their own schedule: [CTAs], each its own copy
   RSeg* segs;       // [W+R]
   RSeg* first;      // [W]   a copy of each worker's first segment, which it reads beside its two numbers
-  int* split_n;     // row blocks in pieces, and
-  int4* split;      // [W] for each: first row, rows, worker of the first piece, pieces (one per worker from there on)
+  int4* split;      // [W] the row block whose first piece is this worker's last segment: first row, rows, -, pieces
+                    // (one per worker from there on); 0 pieces: none
+  int* worker_err;  // [CTAs of the attention kernel] each one's error bits
 };
 
 // The partial slot of piece k of a row block whose first piece is worker w0's:
@@ -54,7 +55,9 @@ struct RaggedSchedArgs {
   int keep_err;            // the error word is an earlier launch's too: do not zero it
   RaggedSched s;
   int* err;
-  int smem_ints;           // words of dynamic shared memory
+  int own;                 // every attention CTA makes its worker's schedule, else ragged_sched_kernel all of it
+  int one_go;              // the latter in one go
+  int smem_ints;           // words of its dynamic shared memory
 };
 
 // Exclusive scan in place, with the total in 64 bits (data[] is meaningless
@@ -142,110 +145,136 @@ struct RaggedShares {
     return (in ? 0 : rest) + (x - (in ? 0 : longer)) / (in ? len + 1 : len);
   }
   // Segment s, piece k of `pieces` of the row block g whose (weighted) tiles
-  // are [v0, v1), owned by worker w; `before`: the worker of segment s - 1.
-  __device__ __forceinline__ void emit(const RaggedSchedArgs& a, RSeg g, int s, int k, int pieces, int v0, int v1, int w,
-                                       int before, bool last) const {
+  // are [v0, v1), owned by worker w; `before`: the worker of
+  // the segment before; `last`: the next one is another worker's.  `range`: where
+  // the worker's segments are noted.
+  __device__ __forceinline__ void emit(const RaggedSched& o, RSeg g, int s, int k, int pieces, int v0, int v1, int w,
+                                       int before, bool last, int2* range) const {
     const int start = v0 + block_tiles;
     g.t_lo = max(share(w) - start, 0);
     g.t_hi = min(share(w + 1), v1) - start;
     // Only the first and the last segment of a worker can be pieces.
     g.slot = pieces == 1 ? -1 : ragged_slot(w - k, k);
     g.pad[0] = g.pad[1] = g.pad[2] = 0;
-    a.s.segs[s] = g;
-    if (before < w) a.s.first[w] = g;
-    for (int v = before + 1; v <= w; ++v) a.s.worker_seg[v] = s;  // shares without a segment start here too
-    if (last)
-      for (int v = w + 1; v <= a.W; ++v) a.s.worker_seg[v] = s + 1;
-    if (k == 0 && pieces > 1) a.s.split[atomicAdd(a.s.split_n, 1)] = make_int4(g.row0, g.nrows, w, pieces);
+    o.segs[s] = g;
+    if (before < w) {
+      o.first[w] = g;
+      range->x = s;
+    }
+    if (last) range->y = s + 1;
+    if (k == 0 && pieces > 1) o.split[w] = make_int4(g.row0, g.nrows, 0, pieces);
   }
 };
 
-// Up to kSchedSmall requests and row blocks take the short way, one per thread
-// with one barrier per sum: the schedule stands at the head of a call that may
-// take 15 us, and cost 6 of them the long way.
-constexpr int kSchedSmall = 512;
+// Where a request's rows start and end and how many keys it sees; false for
+// starts that leave [0, T] or decrease.  A length outside its page table is
+// clamped and sets *range.
+__device__ __forceinline__ bool ragged_request(const RaggedSchedArgs& a, int b, int& s0, int& s1, int& L, int& range) {
+  s0 = a.q_start[b];
+  s1 = a.q_start[b + 1];
+  const long long len = a.kv_len[b], most = a.max_pages * 64LL;
+  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= a.T;
+  if (ok && s1 > s0 && (len < 0 || len > most)) range = 1;
+  L = (int)min(max(len, 0LL), most);
+  return ok;
+}
+__device__ __forceinline__ int ragged_count(const RaggedSchedArgs& a, int s0, int s1) {
+  return (int)(((long long)(s1 - s0) * a.n_h + a.rows - 1) / a.rows);
+}
 
+// The schedule in one go, for up to N requests and row blocks by N threads, with
+// one barrier per sum.  `own`: the worker whose segments are kept, or -1 for all.
+// Where an attention CTA has the threads, it does this for itself: one launch
+// that does it for all, and the wait for it, cost 1 to 3 us (18.1 -> 17.0 for 8
+// requests of one token, 49.0 -> 45.8 for 256; two of each per thread, 0.8 more).
+// Behind that, up to 1024, the schedule kernel does (6 us less than its long way).
+// Segment (row block, worker) has place row block + worker: along the schedule
+// one of the two grows, so the places differ and a worker's are consecutive.
+// `range`: worker max(own, 0)'s entry; the two CTAs of a pair note theirs apart, as
+// one may be done while the other begins.  What else both write is the same.
+// All threads of the block call it.
+template <int N>
+struct RaggedScratch {
+  long long words[2][N / 32];
+  int4 req[N];
+  int bs[N];
+};
+template <int N>
+__device__ __forceinline__ void ragged_schedule(const RaggedSchedArgs& a, RaggedScratch<N>& x, int own, int2* range,
+                                                int* err) {
+  const int tid = threadIdx.x, first = max(own, 0);  // tid: this thread's request and row block
+  for (int w = first + tid; w < (own < 0 ? a.W : own + 1); w += N) {
+    a.s.split[w] = make_int4(0, 0, 0, 0);
+    range[w - first] = make_int2(0, 0);
+  }
+  int n = 0, bad = 0, clamped = 0;
+  if (tid < a.B) {
+    int4 q = make_int4(0, 0, 0, 0);
+    if (ragged_request(a, tid, q.x, q.y, q.z, clamped)) n = ragged_count(a, q.x, q.y);
+    else bad = 1;
+    x.req[tid] = q;
+  }
+  const int none = __syncthreads_or(bad);
+  if (clamped || (none && tid == 0)) flag_error(err, kErrBounds);
+  if (none) return;
+  long long sum;
+  const int first_rb = block_scan_once(n, x.words[0], &sum);
+  const int R = (int)sum;  // at most what the workspace holds: the starts are in order
+  if (tid < a.B) x.bs[tid] = first_rb;
+  __syncthreads();
+  RSeg g{};
+  int v = 0;
+  if (tid < R) {
+    const int b = find_le(x.bs, a.B, tid);
+    const int4 q = x.req[b];
+    g = ragged_block(a, b, tid - x.bs[b], q.x, q.y, q.z);
+    v = ragged_tiles(g) + a.block_tiles;
+  }
+  const int v0 = block_scan_once(v, x.words[1], &sum), v1 = v0 + v;
+  if (R == 0 || sum > 0x7fffffffLL) {
+    if (tid == 0 && R > 0) flag_error(err, kErrBounds);
+    return;
+  }
+  if (tid >= R) return;
+  const RaggedShares sh((int)sum, a.W, a.block_tiles);
+  const int w0 = sh.owner(v0 + a.block_tiles), w1 = sh.owner(v1 - 1);
+  for (int w = own < 0 ? w0 : max(w0, own); w <= (own < 0 ? w1 : min(w1, own)); ++w) {
+    const int before = w > w0 ? w - 1 : (v0 > 0 ? sh.owner(v0 - 1) : -1);
+    const bool last = w < w1 || v1 == sh.total || sh.owner(v1 + a.block_tiles) > w;
+    sh.emit(a.s, g, tid + w, w - w0, w1 - w0 + 1, v0, v1, w, before, last, range + (w - first));
+  }
+}
+
+constexpr int kOneGoMost = 1024;
+
+// The schedule of larger batches, in one launch for all workers.
 __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArgs a) {
-  extern __shared__ int rs_smem[];
-  __shared__ long long words[3][kSchedSmall / 32];
-  __shared__ int bs_s[kSchedSmall + 1], vs_s[kSchedSmall + 1], pc_s[kSchedSmall + 1], wf_s[kSchedSmall];
-  __shared__ int4 req[kSchedSmall];
-  __shared__ RSeg blocks[kSchedSmall];
+  extern __shared__ __align__(16) int rs_smem[];
   const int tid = threadIdx.x, nt = blockDim.x;
   sm100::pdl_wait();
   sm100::pdl_trigger();
-  if (tid == 0) {
-    if (!a.keep_err) *a.err = 0;
-    *a.s.split_n = 0;
+  if (tid == 0 && !a.keep_err) *a.err = 0;
+  if (a.one_go) {
+    __syncthreads();  // the error word is zero
+    ragged_schedule<kOneGoMost>(a, *reinterpret_cast<RaggedScratch<kOneGoMost>*>(rs_smem), -1, a.s.range, a.err);
+    return;
   }
-  // Starts that leave [0, T] or decrease leave nothing to compute; a length
-  // outside its page table is clamped.
-  const bool small = a.B <= nt && nt <= kSchedSmall;
-  int* const bs = small ? bs_s : rs_smem;  // [B+1] first row block of each request
+  for (int w = tid; w < a.W; w += nt) {
+    a.s.split[w] = make_int4(0, 0, 0, 0);
+    a.s.range[w] = make_int2(0, 0);
+  }
+  int* const off = rs_smem;  // [B+1] first row block of each request
   int bad = 0, range = 0;
   for (int b = tid; b < a.B; b += nt) {
-    const int s0 = a.q_start[b], s1 = a.q_start[b + 1], L = a.kv_len[b];
-    const bool ok = s0 >= 0 && s1 >= s0 && s1 <= a.T;
-    const long long most = a.max_pages * 64LL;
+    int s0, s1, L;
+    const bool ok = ragged_request(a, b, s0, s1, L, range);
     if (!ok) bad = 1;
-    if (ok && s1 > s0 && (L < 0 || L > most)) range = 1;
-    bs[b] = ok ? (int)(((long long)(s1 - s0) * a.n_h + a.rows - 1) / a.rows) : 0;
-    if (small) req[b] = make_int4(s0, s1, (int)min(max((long long)L, 0LL), most), 0);
+    off[b] = ok ? ragged_count(a, s0, s1) : 0;
   }
   const int none = __syncthreads_or(bad);
   if (range || (none && tid == 0)) flag_error(a.err, kErrBounds);
-  if (none) {
-    for (int w = tid; w <= a.W; w += nt) a.s.worker_seg[w] = 0;
-    return;
-  }
+  if (none) return;
 
-  if (small) {
-    long long sum;
-    const int n_blocks = tid < a.B ? bs[tid] : 0, first_rb = block_scan_once(n_blocks, words[0], &sum);
-    const int R = (int)sum;  // at most the workspace's row blocks, for which there are threads
-    if (tid < a.B) bs[tid] = first_rb;
-    __syncthreads();
-    const bool mine = tid < R;
-    RSeg g{};
-    int v = 0;
-    if (mine) {
-      const int b = find_le(bs, a.B, tid);
-      const int4 q = req[b];
-      g = ragged_block(a, b, tid - bs[b], q.x, q.y, q.z);
-      v = ragged_tiles(g) + a.block_tiles;
-      blocks[tid] = g;
-    }
-    const int v0 = block_scan_once(v, words[1], &sum);
-    if (R == 0 || sum > 0x7fffffffLL) {
-      if (tid == 0 && R > 0) flag_error(a.err, kErrBounds);
-      for (int w = tid; w <= a.W; w += nt) a.s.worker_seg[w] = 0;
-      return;
-    }
-    const RaggedShares sh((int)sum, a.W, a.block_tiles);
-    int pieces = 0;
-    if (mine) {
-      const int w0 = sh.owner(v0 + a.block_tiles);
-      pieces = sh.owner(v0 + v - 1) - w0 + 1;
-      wf_s[tid] = w0;
-      vs_s[tid] = v0;
-    }
-    const int s0 = block_scan_once(pieces, words[2], &sum);
-    if (mine) pc_s[tid] = s0;
-    const int nseg = (int)sum;
-    if (tid == 0) {
-      pc_s[R] = nseg;
-      vs_s[R] = sh.total;
-    }
-    __syncthreads();
-    for (int s = tid; s < nseg; s += nt) {
-      const int rb = find_le(pc_s, R, s), k = s - pc_s[rb], w = wf_s[rb] + k;
-      const int before = k > 0 ? w - 1 : (rb > 0 ? wf_s[rb - 1] + s - pc_s[rb - 1] - 1 : -1);
-      sh.emit(a, blocks[rb], s, k, pc_s[rb + 1] - pc_s[rb], vs_s[rb], vs_s[rb + 1], w, before, s == nseg - 1);
-    }
-    return;
-  }
-
-  int* const off = rs_smem;
   const int R = (int)ragged_scan(off, a.B);  // at most what the workspace holds: the starts are in order
   if (tid == 0) off[a.B] = R;
   const bool in_smem = a.B + 1 + 3 * (R + 1) <= a.smem_ints;
@@ -255,15 +284,15 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   __syncthreads();
   auto block = [&](int rb) {
     const int b = find_le(off, a.B, rb);
-    return ragged_block(a, b, rb - off[b], a.q_start[b], a.q_start[b + 1],
-                        (int)min(max((long long)a.kv_len[b], 0LL), a.max_pages * 64LL));
+    int s0, s1, L, clamped;
+    ragged_request(a, b, s0, s1, L, clamped);
+    return ragged_block(a, b, rb - off[b], s0, s1, L);
   };
   for (int rb = tid; rb < R; rb += nt) vs[rb] = ragged_tiles(block(rb)) + a.block_tiles;
   __syncthreads();
   const long long total = ragged_scan(vs, R);
   if (R == 0 || total > 0x7fffffffLL) {
     if (tid == 0 && R > 0) flag_error(a.err, kErrBounds);
-    for (int w = tid; w <= a.W; w += nt) a.s.worker_seg[w] = 0;
     return;
   }
   if (tid == 0) vs[R] = (int)total;
@@ -280,7 +309,8 @@ __global__ void __launch_bounds__(1024) ragged_sched_kernel(const RaggedSchedArg
   for (int s = tid; s < nseg; s += nt) {
     const int rb = find_le(pc, R, s), k = s - pc[rb], w = wf[rb] + k;
     const int before = k > 0 ? w - 1 : (rb > 0 ? wf[rb - 1] + s - pc[rb - 1] - 1 : -1);
-    sh.emit(a, block(rb), s, k, pc[rb + 1] - pc[rb], vs[rb], vs[rb + 1], w, before, s == nseg - 1);
+    sh.emit(a.s, block(rb), s, k, pc[rb + 1] - pc[rb], vs[rb], vs[rb + 1], w, before,
+            s == nseg - 1 || k + 1 < pc[rb + 1] - pc[rb] || wf[rb + 1] > w, a.s.range + w);
   }
 }
 
@@ -312,11 +342,13 @@ __device__ __forceinline__ float row_lse(float ref, float l) { return l == 0.f ?
 // and sum are brought up to date in shared memory as an online softmax does,
 // and the batch is added.  Bound by latency (some pieces of a few hundred KB
 // in all, from L2), hence one pass: about 4 us for eight row blocks of nine
-// pieces.
+// pieces.  The first CTA also gathers the attention CTAs' error bits into the
+// call's error word (`keep_err`: beside what an earlier launch left there).
 constexpr int kCombineCols = 16, kCombineThreads = 128, kBatch = 4;
 
 template <typename T, int ROWS, bool kByColumn>
-__global__ void __launch_bounds__(kCombineThreads) ragged_combine_kernel(RaggedSched S, RaggedOut o) {
+__global__ void __launch_bounds__(kCombineThreads) ragged_combine_kernel(RaggedSched S, RaggedOut o, int err_ctas, int* err,
+                                                                         int keep_err) {
   sm100::pdl_wait();
   sm100::pdl_trigger();
   constexpr int QUADS = ROWS * kCombineCols / 4 / kCombineThreads;  // 16-byte items per thread
@@ -325,9 +357,15 @@ __global__ void __launch_bounds__(kCombineThreads) ragged_combine_kernel(RaggedS
   __shared__ float tile[kByColumn ? ROWS : 1][kCombineCols + 1];
   __shared__ float inv_of[ROWS];
   const int tid = threadIdx.x;
-  const int4 e = S.split[blockIdx.x];  // asked for before the count is known
-  if ((int)blockIdx.x >= *S.split_n) return;
-  const int row0 = e.x, nrows = e.y, w0 = e.z, np = e.w;
+  const int4 e = S.split[blockIdx.x];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid < 32) {
+    int bits = 0;
+    for (int i = tid; i < err_ctas; i += 32) bits |= S.worker_err[i];
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (tid == 0) *err = bits | (keep_err ? *err : 0);
+  }
+  const int row0 = e.x, nrows = e.y, w0 = blockIdx.x, np = e.w;
+  if (np == 0) return;
   const int col0 = blockIdx.y * kCombineCols, cols = min(kCombineCols, o.d_c - col0);
   const int pitch = kByColumn ? o.d_c : (o.d_c + 3) & ~3;
   const long long slot_elems = (long long)pitch * ROWS;

@@ -657,6 +657,43 @@ def test_attend_ragged_schedules_of_many_requests_and_row_blocks(mla, dtype, n_h
     s.check(out, lse, only=list(r.choice(B, 12, replace=False)) + [0, B - 1])
 
 
+@pytest.mark.parametrize("by", ["requests", "row blocks"])
+@pytest.mark.parametrize("dtype,most", [("bf16", 384), ("bf16", 385), ("bf16", 1024), ("bf16", 1025), ("f32", 256),
+                                        ("f32", 257), ("f32", 1024), ("f32", 1025)])
+def test_attend_ragged_at_the_limits_of_each_way_to_schedule(mla, dtype, most, by):
+    """At one more than these numbers another kernel, or another part of it, makes the schedule."""
+    r = np.random.default_rng(most)
+    if by == "requests":                       # most of them without a token, the longest ones at both ends
+        n_h, lens = 4, [(0, int(k)) for k in r.integers(0, 100, most)]
+        for b in r.choice(most, 30, replace=False):
+            lens[b] = (int(r.integers(1, 4)), int(r.integers(3, 200)))
+        lens[0], lens[-1] = (2, 1900), (1, 2100)
+    else:                                      # one row block per token, and two requests
+        n_h = 128 if dtype == "bf16" else 64
+        lens = [(most - 2 - 7, most + 40), (7, 900)]
+    s = Step(mla, dtype, n_h, 128, 16, lens)
+    only = [0, s.B - 1] + ([b for b in range(s.B) if s.new[b]][1:8] if by == "requests" else [])
+    first = s.run()
+    s.check(*first, only=only)
+    good = s.table.clone()
+    s.table[-1, 1] = 10 ** 6                   # a page that is not there: reported, and by this call alone
+    s.run()
+    torch.cuda.synchronize()
+    assert mla.get_error(s.ws) == -5
+    s.table.copy_(good)
+    again = s.run()
+    s.check(*again, only=only)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    s.kv[-1] += 64 * s.table.shape[1]          # a length behind the table
+    s.run()
+    torch.cuda.synchronize()
+    assert mla.get_error(s.ws) == -5
+    s.starts[1], s.starts[2] = s.starts[2] + 1, s.starts[1]
+    out, lse = s.run()
+    torch.cuda.synchronize()
+    assert mla.get_error(s.ws) == -5 and (out == 7).all() and (lse == 7).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attend_ragged_schedule_that_does_not_fit_shared_memory(mla, dtype):
     """16,000 requests of one token and 64 heads or more are more row blocks than the schedule keeps on chip."""
