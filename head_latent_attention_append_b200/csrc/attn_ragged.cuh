@@ -204,6 +204,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   pdl_wait();
   pdl_trigger();
   const RSeg* segs = a.sched.s.segs;
+  // The worker's segments pass through memory either way: handed over in
+  // registers, they cost the page loop 2 to 4%.
   int2* const range = a.sched.s.range + (a.sched.own ? blockIdx.x : w);
   if (a.sched.own) {
     ragged_schedule<kOwnMost>(a.sched, *reinterpret_cast<RaggedScratch<kOwnMost>*>(smem + OFF_VG), w, range, err);
