@@ -123,12 +123,17 @@ __device__ __forceinline__ void run_segment(const Args& a, const Ctx& x, const R
     if (k0 + KT < k_end) page_next = pages[(k0 + KT) / 64];
   };
   __syncthreads();  // the segment before is done with Qs and the key tiles
+  // A block without keys needs no query rows either, and must not ask for them:
+  // the key loop holds the only wait for the copies, and ones still in flight
+  // could land on the next segment's rows.
+  if (k_begin < k_end) {
 #pragma unroll 1
-  for (int i = 0; i < MI; ++i) {
-    const int r = warp + WARPS * i, row = g.row0 + min(r, g.nrows - 1), t = row / a.n_h;
-    put_row(a, x, x.Qs + r * P4, a.q + t * a.q_ts + (row - t * a.n_h) * a.q_hs, r < g.nrows, lane);
+    for (int i = 0; i < MI; ++i) {
+      const int r = warp + WARPS * i, row = g.row0 + min(r, g.nrows - 1), t = row / a.n_h;
+      put_row(a, x, x.Qs + r * P4, a.q + t * a.q_ts + (row - t * a.n_h) * a.q_hs, r < g.nrows, lane);
+    }
+    fetch(k_begin, x.Kb);
   }
-  if (k_begin < k_end) fetch(k_begin, x.Kb);
   // The softmax state of the warp's rows: four lanes each, row lane / 4 (a warp
   // of fewer than eight rows leaves the others at no key).
   const int sr = lane >> 2, my_row = warp + WARPS * sr;
