@@ -247,6 +247,14 @@ struct Vec {
       ss = __ffma2_rn(f[e], f[e], ss);
     }
   }
+  // Times a power of two (exact, but for results below the type's normal range).
+  __device__ __forceinline__ void scale(float by) {
+    float2 f[NP];
+    get(f);
+#pragma unroll
+    for (int e = 0; e < NP; ++e) f[e] = __fmul2_rn(f[e], make_float2(by, by));
+    set(f);
+  }
   // The normalised values: x * inv * gamma, rounded once.
   __device__ __forceinline__ void norm(float inv, const Vec& g) {
     float2 f[NP], h[NP];
@@ -338,22 +346,30 @@ struct RowPart {
   // RMS norm: out = x / sqrt(mean(x^2) + eps) * gamma in 32 bits, rounded once;
   // a null gamma copies the row.  `x` and `out` may be the same row; `g` is
   // this thread's share of gamma.  Where the sum of squares passes the range
-  // of 32 bits it is taken again of x 2^-64.  `live` is false in threads that
-  // only take part in the sums.
+  // of 32 bits it is taken again of x 2^-96, so that no row of finite values
+  // passes it (2^64 per value); 1 / sqrt(mean) is then as small as 2^-128,
+  // below the normal range, so x takes 2^-64 of it and the factor the rest.
+  // `live` is false in threads that only take part in the sums.
   template <class Total>
   __device__ __forceinline__ void norm(const RowPart& g, const T* x, const T* gamma, T* out, int nv, float inv_n,
                                        float eps, int lane, int lanes, bool live, const Total& total) {
     float inv = 1.f;
+    bool far = false;
     if (gamma) {  // the same for every row
       const int own = live ? nv : 0;
       const float ss = total(squares<false>(x, own, lane, lanes, 1.f));
       inv = rsqrtf(fmaf(ss, inv_n, eps));
-      if (total.any(isinf(ss))) {
-        const float small = total(squares<true>(x, own, lane, lanes, 0x1p-64f));
-        if (isinf(ss)) inv = rsqrtf(fmaf(small, inv_n, eps * 0x1p-64f * 0x1p-64f)) * 0x1p-64f;
+      far = isinf(ss);
+      if (total.any(far)) {
+        const float small = total(squares<true>(x, own, lane, lanes, 0x1p-96f));
+        if (far) inv = rsqrtf(fmaf(small, inv_n, eps * 0x1p-96f * 0x1p-96f)) * 0x1p-32f;
       }
     }
     if (!live) return;
+    if (far) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i].scale(0x1p-64f);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (lane + lanes * i < nv) {
@@ -365,6 +381,7 @@ struct RowPart {
       u.load(x + i * V::VE);
       if (gamma) {
         w.load(gamma + i * V::VE);
+        if (far) u.scale(0x1p-64f);
         u.norm(inv, w);
       }
       u.store(out + i * V::VE);

@@ -5,7 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_ragged import Step, mla  # noqa: E402,F401  (the fixture)
+from test_gpu_ragged import DEV, DT, Step, close_norm, dims_of, gen, i32, mla, randn, rms64  # noqa: E402,F401
 
 
 # ------------------------------------------------------------------ attention
@@ -42,3 +42,52 @@ def test_attend_ragged_row_blocks_without_keys_between_others(mla, B, n_h, d_c, 
     s.check(*first)
     for _ in range(5):
         assert all(torch.equal(a, b) for a, b in zip(first, s.run()))
+
+
+# ---------------------------------------------------------------------- norms
+# Widths that the threads hold in registers, longer ones, odd ones: dtype, d_c, d_cq, d_h.
+NORM_WIDTHS = [("bf16", 512, 1536, 128), ("bf16", 128, 9000, 1504), ("f32", 64, 96, 32), ("f32", 512, 4100, 1028),
+               ("f32", 5, 513, 131)]
+
+
+def check_norms(mla, dtype, d_c, d_cq, d_h, scales, eps):
+    """Both norm calls on rows (and, in the query call, heads) of these scales, one behind the other."""
+    g, T, n_h, d_r = gen(d_c), len(scales), 3, 16 if dtype == "bf16" else 2
+    dims = dims_of(mla, dtype, n_h, d_h, d_c, d_r, d_cq)
+    factor = torch.tensor(scales, device=DEV)[:, None]
+    rows = lambda n: (torch.rand(T, n, generator=g, device=DEV) * 2 - 1).mul(factor).to(DT[dtype])
+    kv, cq = rows(d_c + d_r), rows(d_cq)
+    gk, gq, gh = (randn(g, n, dtype=DT[dtype]) for n in (d_c, d_cq, d_h))
+    assert all(torch.isfinite(x).all() for x in (kv, cq))
+    pos = i32(range(T))
+    cache, out = torch.zeros(1, 64, d_c + d_r, dtype=DT[dtype], device=DEV), torch.empty_like(cq)
+    mla.append_normed(dims, kv, gk, pos, torch.arange(T, device=DEV), cache, eps, cq, gq, out)
+    close_norm(cache[0, :T, :d_c], rms64(kv[:, :d_c], gk, eps), dtype, d_c)
+    close_norm(out, rms64(cq, gq, eps), dtype, d_cq)
+    # Heads of different scales share a warp.
+    q = torch.stack([rows(d_h + d_r).roll(h, 0) for h in range(n_h)], 1).contiguous()
+    qc, qr = torch.empty(T, n_h, d_h, dtype=DT[dtype], device=DEV), torch.empty(T, n_h, d_r, dtype=DT[dtype], device=DEV)
+    mla.query_norm_rope(dims, q, gh, pos, qc, qr, eps)
+    close_norm(qc, rms64(q[..., :d_h], gh, eps), dtype, d_h)
+
+
+@pytest.mark.parametrize("dtype,d_c,d_cq,d_h", NORM_WIDTHS)
+def test_norms_of_rows_whose_squares_pass_32_bits(mla, dtype, d_c, d_cq, d_h):
+    check_norms(mla, dtype, d_c, d_cq, d_h, [1.0, 3e18, 1e37, 1e38, 3.3e38, 1e-3, 2e19, 3.3e38], 1e-6)
+
+
+@pytest.mark.parametrize("dtype,d_c,d_cq,d_h", NORM_WIDTHS)
+def test_norms_of_rows_of_the_largest_value(mla, dtype, d_c, d_cq, d_h):
+    """Every value of the row as large as the type holds: outputs of +-gamma."""
+    most, d_r = torch.finfo(DT[dtype]).max, 16 if dtype == "bf16" else 2
+    dims = dims_of(mla, dtype, 1, d_h, d_c, d_r, d_cq)
+    ones = lambda n: torch.ones(n, dtype=DT[dtype], device=DEV)
+    kv, cq, q = (torch.full((1, n), most, dtype=DT[dtype], device=DEV) for n in (d_c + d_r, d_cq, d_h + d_r))
+    kv[0, 1::2] = -most
+    cache, out = torch.zeros(1, 64, d_c + d_r, dtype=DT[dtype], device=DEV), torch.empty_like(cq)
+    mla.append_normed(dims, kv, ones(d_c), i32([0]), torch.tensor([5], device=DEV), cache, 1e-6, cq, ones(d_cq), out)
+    close_norm(cache[0, 5:6, :d_c], rms64(kv[:, :d_c], ones(d_c), 1e-6), dtype, d_c)
+    close_norm(out, rms64(cq, ones(d_cq), 1e-6), dtype, d_cq)
+    qc, qr = torch.empty(1, 1, d_h, dtype=DT[dtype], device=DEV), torch.empty(1, 1, d_r, dtype=DT[dtype], device=DEV)
+    mla.query_norm_rope(dims, q.view(1, 1, -1), ones(d_h), i32([0]), qc, qr)
+    close_norm(qc, rms64(q[:, None, :d_h], ones(d_h), 1e-6), dtype, d_h)
