@@ -349,26 +349,32 @@ struct RowPart {
   // of 32 bits it is taken again of x 2^-96, so that no row of finite values
   // passes it (2^64 per value); 1 / sqrt(mean) is then as small as 2^-128,
   // below the normal range, so x takes 2^-64 of it and the factor the rest.
+  // Where the squares fall below that range (and eps is too small to matter
+  // less than they do) the same is done with 2^96, 2^64 and 2^32.
   // `live` is false in threads that only take part in the sums.
   template <class Total>
   __device__ __forceinline__ void norm(const RowPart& g, const T* x, const T* gamma, T* out, int nv, float inv_n,
                                        float eps, int lane, int lanes, bool live, const Total& total) {
     float inv = 1.f;
+    float part = 1.f;
     bool far = false;
     if (gamma) {  // the same for every row
       const int own = live ? nv : 0;
       const float ss = total(squares<false>(x, own, lane, lanes, 1.f));
-      inv = rsqrtf(fmaf(ss, inv_n, eps));
-      far = isinf(ss);
+      const float mean = fmaf(ss, inv_n, eps);
+      inv = rsqrtf(mean);
+      far = isinf(ss) || mean < 0x1p-100f;
       if (total.any(far)) {
-        const float small = total(squares<true>(x, own, lane, lanes, 0x1p-96f));
-        if (far) inv = rsqrtf(fmaf(small, inv_n, eps * 0x1p-96f * 0x1p-96f)) * 0x1p-32f;
+        const float by = isinf(ss) ? 0x1p-96f : 0x1p96f;
+        const float again = total(squares<true>(x, own, lane, lanes, by));
+        if (far) inv = rsqrtf(fmaf(again, inv_n, eps * by * by)) * (isinf(ss) ? 0x1p-32f : 0x1p32f);
+        part = isinf(ss) ? 0x1p-64f : 0x1p64f;
       }
     }
     if (!live) return;
     if (far) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i].scale(0x1p-64f);
+      for (int i = 0; i < NV; ++i) v[i].scale(part);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -381,7 +387,7 @@ struct RowPart {
       u.load(x + i * V::VE);
       if (gamma) {
         w.load(gamma + i * V::VE);
-        if (far) u.scale(0x1p-64f);
+        if (far) u.scale(part);
         u.norm(inv, w);
       }
       u.store(out + i * V::VE);

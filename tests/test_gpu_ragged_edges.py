@@ -91,3 +91,10 @@ def test_norms_of_rows_of_the_largest_value(mla, dtype, d_c, d_cq, d_h):
     qc, qr = torch.empty(1, 1, d_h, dtype=DT[dtype], device=DEV), torch.empty(1, 1, d_r, dtype=DT[dtype], device=DEV)
     mla.query_norm_rope(dims, q.view(1, 1, -1), ones(d_h), i32([0]), qc, qr)
     close_norm(qc, rms64(q[:, None, :d_h], ones(d_h), 1e-6), dtype, d_h)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-35])
+@pytest.mark.parametrize("dtype,d_c,d_cq,d_h", NORM_WIDTHS)
+def test_norms_of_rows_whose_squares_fall_below_32_bits(mla, dtype, d_c, d_cq, d_h, eps):
+    """A small or no eps: what the squares lose of their bits shows.  Rows of ordinary size beside them."""
+    check_norms(mla, dtype, d_c, d_cq, d_h, [1e-18, 1.0, 1e-25, 1e-30, 3e-20, 1e-34, 1e38, 1e-16], eps)
