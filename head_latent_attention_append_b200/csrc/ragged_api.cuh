@@ -56,6 +56,55 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return na && nb && x < y + nb && y < x + na;
 }
 
+// The bytes of a tensor of rows: n groups s bytes apart, each of m rows of w
+// bytes hs apart (rows do not overlap and come in order).
+struct RowSet {
+  uintptr_t p;
+  long long n, s, m, hs, w;
+  uintptr_t end;  // behind the last row (0 where there are no rows)
+  RowSet(const void* p_, long long n_, long long s_, long long m_, long long hs_, long long w_)
+      : p(reinterpret_cast<uintptr_t>(p_)), n(n_), s(s_), m(m_), hs(hs_), w(w_), end(n ? p + (n - 1) * s + extent() : 0) {}
+  RowSet(const void* p_, long long bytes) : RowSet(p_, p_ && bytes ? 1 : 0, bytes, 1, bytes, bytes) {}
+  long long extent() const { return (m - 1) * hs + w; }
+};
+bool same_rows(const RowSet& a, const RowSet& b) {
+  return a.p == b.p && a.n == b.n && a.m == b.m && a.w == b.w && (a.n <= 1 || a.s == b.s) && (a.m <= 1 || a.hs == b.hs);
+}
+// Whether a group of `a` and one of `b` that starts `d` bytes behind it share a byte.
+bool groups_meet(const RowSet& a, const RowSet& b, long long d) {
+  for (long long i = 0, j = 0; i < a.m && j < b.m;) {
+    const long long x = i * a.hs, y = d + j * b.hs;
+    if (x < y + b.w && y < x + a.w) return true;
+    if (x < y) ++i;
+    else ++j;
+  }
+  return false;
+}
+// Whether two tensors with rows share a byte.  Interleaved ones (slices of one
+// wider row) do not; they have one stride, for which a few groups tell of all.
+__attribute__((noinline)) bool rows_cross(RowSet a, RowSet b) {
+  const long long d = (long long)(b.p - a.p), ea = a.extent(), eb = b.extent();
+  if (a.n == 1) a.s = b.s;
+  if (b.n == 1) b.s = a.s;
+  if (a.s == b.s) {
+    // Group j of b against group j - k of a: d + k s bytes apart.
+    const long long first = (-eb - d) / a.s - 1;
+    for (long long k = std::max(1 - a.n, first); k < b.n && d + k * a.s < ea; ++k)
+      if (d + k * a.s > -eb && groups_meet(a, b, d + k * a.s)) return true;
+    return false;
+  }
+  for (long long i = 0, j = 0; i < a.n && j < b.n;) {
+    const long long x = i * a.s, y = d + j * b.s;
+    if (x < y + eb && y < x + ea && groups_meet(a, b, y - x)) return true;
+    if (x + ea < y + eb) ++i;
+    else ++j;
+  }
+  return false;
+}
+// The same for any two: tensors apart, the usual case, cost two comparisons
+// (all of a call's together some tens of nanoseconds).
+inline bool rows_meet(const RowSet& a, const RowSet& b) { return a.p < b.end && b.p < a.end && rows_cross(a, b); }
+
 // RoPE frequencies as turns per position.
 step::Rope rope_table(const mla_dims& d) {
   static thread_local step::Rope last;
@@ -317,6 +366,19 @@ mla_status mla_append_normed(const mla_dims* dims, const void* kv, int64_t kv_st
   if (!aligned(kv, e) || !aligned(kv_gamma, e) || !aligned(cq, e) || !aligned(cq_gamma, e) || !aligned(cq_out, e) ||
       !aligned(pos, 4) || !aligned(slot, 8) || !aligned(cache, 16) || !aligned(device_error, 4))
     return MLA_ERR_INVALID_ARG;
+  {
+    // Other blocks still read their rows while this one writes: only a c_Q row
+    // may be written over itself.
+    const long long b = (long long)e;
+    const RowSet rows(kv, T, kv_stride * b, 1, 0, d_cr * b), latent(cq, cq ? T : 0, cq_stride * b, 1, 0, d.d_cq * b),
+        out(cq_out, cq ? T : 0, cq_out_stride * b, 1, 0, d.d_cq * b),
+        pages(cache, (long long)num_pages * d.page_size * d_cr * b);
+    const RowSet in[] = {rows, {kv_gamma, d.d_c * b}, {cq_gamma, d.d_cq * b}, {pos, 4LL * T}, {slot, 8LL * T}};
+    for (const RowSet& x : in)
+      if (rows_meet(x, pages) || rows_meet(x, out)) return MLA_ERR_INVALID_ARG;
+    if (rows_meet(latent, pages) || rows_meet(out, pages) || (rows_meet(latent, out) && !same_rows(latent, out)))
+      return MLA_ERR_INVALID_ARG;
+  }
   step::NormAppendArgs a{};
   a.kv = kv; a.kv_gamma = kv_gamma; a.kv_stride = kv_stride;
   a.cq = cq; a.cq_gamma = cq_gamma; a.cq_stride = cq_stride;
@@ -353,6 +415,20 @@ mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_st
   const size_t e = esize(d);
   if (!aligned(q, e) || !aligned(gamma, e) || !aligned(pos, 4) || !aligned(qc_out, e) || !aligned(qr_out, e))
     return MLA_ERR_INVALID_ARG;
+  {
+    // As in the append: a part of q may only be written over itself.
+    const long long b = (long long)e, dq = (d.d_h + d.d_r) * b;
+    const RowSet content(q, T, q_stride * b, d.n_h, dq, d.d_h * b),
+        position(static_cast<const char*>(q) + d.d_h * b, T, q_stride * b, d.n_h, dq, d.d_r * b),
+        qc(qc_out, T, qc_token_stride * b, d.n_h, qc_head_stride * b, d.d_h * b),
+        qr(qr_out, T, qr_token_stride * b, d.n_h, qr_head_stride * b, d.d_r * b);
+    const RowSet in[] = {{gamma, d.d_h * b}, {pos, 4LL * T}};
+    for (const RowSet& x : in)
+      if (rows_meet(x, qc) || rows_meet(x, qr)) return MLA_ERR_INVALID_ARG;
+    if (rows_meet(qc, qr) || rows_meet(content, qr) || rows_meet(position, qc) ||
+        (rows_meet(content, qc) && !same_rows(content, qc)) || (rows_meet(position, qr) && !same_rows(position, qr)))
+      return MLA_ERR_INVALID_ARG;
+  }
   const int ve = 16 / (int)e;
   const bool vec = aligned(q, 16) && aligned(gamma, 16) && aligned(qc_out, 16) && aligned(qr_out, 16) &&
                    d.d_h % ve == 0 && d.d_r % ve == 0 && q_stride % ve == 0 && qc_token_stride % ve == 0 &&

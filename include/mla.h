@@ -356,8 +356,9 @@ mla_status mla_plan_step(const int32_t* new_len, const int32_t* past_len, int B,
  * an unrotated position key, [c | k_R]; writes
  *   cache row slot[t] = [c / sqrt(mean(c^2) + eps) * kv_gamma | RoPE_pos[t](k_R)]
  * and, when cq is given, cq_out[t] = cq[t] / sqrt(mean(cq[t]^2) + eps) *
- * cq_gamma (d_cq elements; strides in elements; cq_out may be cq).  A NULL
- * gamma leaves that latent unnormalised.  Statistics, rotation and products are
+ * cq_gamma (d_cq elements; strides in elements; cq_out may be cq, with cq's
+ * stride; any other overlap of an output with an input or the other output is
+ * MLA_ERR_INVALID_ARG).  A NULL gamma leaves that latent unnormalised.  Statistics, rotation and products are
  * taken in 32 bits (angles in 64) and rounded once.  slot -1 leaves the cache
  * alone; any other slot outside [0, num_pages*64) does too and ORs 1 into
  * *device_error (may be NULL).  Slots other than -1 must differ.  Rows that
@@ -376,7 +377,8 @@ mla_status mla_append_normed(const mla_dims* dims, const void* kv, int64_t kv_st
  *   qr_out[t, h] = RoPE_pos[t](q_R),
  * each with its own token and head strides (elements), so q_R can go straight
  * into the [q~ | q_R] rows that the attention reads.  Outputs may be the same
- * parts of q itself (same addresses and strides).  Rounded once, as above. */
+ * parts of q itself (same addresses and strides); any other overlap is
+ * MLA_ERR_INVALID_ARG.  Rounded once, as above. */
 mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_stride,
                                const void* gamma, float eps, const int32_t* pos, void* qc_out,
                                int64_t qc_token_stride, int64_t qc_head_stride, void* qr_out,

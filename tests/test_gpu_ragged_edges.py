@@ -5,7 +5,8 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_ragged import DEV, DT, Step, close_norm, dims_of, gen, i32, mla, randn, rms64  # noqa: E402,F401
+from test_gpu_ragged import (DEV, DT, Step, close_norm, close_turn, dims_of, gen, i32, mla, randn, rms64,  # noqa: E402,F401
+                             turn64)
 
 
 # ------------------------------------------------------------------ attention
@@ -98,3 +99,51 @@ def test_norms_of_rows_of_the_largest_value(mla, dtype, d_c, d_cq, d_h):
 def test_norms_of_rows_whose_squares_fall_below_32_bits(mla, dtype, d_c, d_cq, d_h, eps):
     """A small or no eps: what the squares lose of their bits shows.  Rows of ordinary size beside them."""
     check_norms(mla, dtype, d_c, d_cq, d_h, [1e-18, 1.0, 1e-25, 1e-30, 3e-20, 1e-34, 1e38, 1e-16], eps)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 3, 700])
+def test_append_writes_the_query_latent_over_itself_beside_the_rows_of_the_cache(mla, dtype, T):
+    """One wide row holds c_Q, the latent and the key: in place, and into another part of the same rows."""
+    g, d_c, d_r, d_cq = gen(T), 128, 16, 200
+    dims = dims_of(mla, dtype, 2, 32, d_c, d_r, d_cq)
+    ones = lambda n: torch.ones(n, dtype=DT[dtype], device=DEV)
+    pos, slot = i32(range(T)), torch.randperm(-(-T // 64) * 64, generator=g, device=DEV)[:T].contiguous()
+    for place in (0, d_cq + d_c + d_r):                       # over itself; behind the key
+        wide = randn(g, T, 2 * d_cq + d_c + d_r, dtype=DT[dtype])
+        keep = wide.clone()
+        cq, kv, out = wide[:, :d_cq], wide[:, d_cq:d_cq + d_c + d_r], wide[:, place:place + d_cq]
+        cache = torch.zeros(-(-T // 64), 64, d_c + d_r, dtype=DT[dtype], device=DEV)
+        mla.append_normed(dims, kv, ones(d_c), pos, slot, cache, 1e-6, cq, ones(d_cq), out)
+        close_norm(out, rms64(keep[:, :d_cq], ones(d_cq), 1e-6), dtype, d_cq)
+        close_norm(cache.view(-1, d_c + d_r)[slot, :d_c], rms64(keep[:, d_cq:d_cq + d_c], ones(d_c), 1e-6), dtype, d_c)
+        same = torch.ones(wide.shape[1], dtype=torch.bool, device=DEV)
+        same[place:place + d_cq] = False
+        assert torch.equal(wide[:, same], keep[:, same])
+        if T > 1:
+            with pytest.raises(mla.MlaError) as e:            # c_Q's rows, packed: where other rows still are
+                mla.append_normed(dims, kv, ones(d_c), pos, slot, cache, 1e-6, cq, ones(d_cq),
+                                  torch.as_strided(wide, (T, d_cq), (d_cq, 1)))
+            assert e.value.code == -1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,n_h", [(1, 1), (1, 5), (40, 1), (40, 7)])
+def test_query_outputs_in_other_parts_of_the_rows_of_q(mla, dtype, T, n_h):
+    """Rows [q_C | q_R of all heads | room for the outputs]: head strides differ, token strides do not."""
+    g, d_h, d_r = gen(T + n_h), 32, 16
+    dims, dq = dims_of(mla, dtype, n_h, d_h, 128, d_r), d_h + d_r
+    gamma, pos = randn(g, d_h, dtype=DT[dtype]), i32([5 * i for i in range(T)])
+    wide = randn(g, T, 2 * n_h * dq, dtype=DT[dtype])
+    keep = wide.clone().view(T, 2, n_h, dq)[:, 0]
+    view = lambda n, at, hs: torch.as_strided(wide, (T, n_h, n), (wide.shape[1], hs, 1), at)
+    q, qc, qr = view(dq, 0, dq), view(d_h, n_h * dq, d_h), view(d_r, n_h * (dq + d_h), d_r)
+    mla.query_norm_rope(dims, q, gamma, pos, qc, qr, 1e-6)
+    close_norm(qc, rms64(keep[..., :d_h], gamma, 1e-6), dtype, d_h)
+    close_turn(qr, turn64(keep[..., d_h:], pos), keep[..., d_h:], dtype)
+    assert torch.equal(q, keep)
+    if n_h > 1:
+        for bad in (dict(qc_out=view(d_h, 0, d_h)), dict(qr_out=view(d_r, d_h, d_r)), dict(qr_out=qc[..., :d_r])):
+            with pytest.raises(mla.MlaError) as e:
+                mla.query_norm_rope(dims, q, gamma, pos, **{"qc_out": qc, "qr_out": qr, **bad})
+            assert e.value.code == -1

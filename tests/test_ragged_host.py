@@ -165,3 +165,32 @@ def test_ragged_step_refusals_and_sizes(mla):
     assert mla.ragged_step_workspace_bytes(dims(mla, rope_key_per_head=1, d_c=128), 4, 70) == 0
     # A null handle is refused before anything else is looked at.
     assert mla.lib.mla_ragged_step(None, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 9, FAKE, FAKE, 4, 70, FAKE, need, None) == INVALID
+
+
+def test_append_and_query_refuse_outputs_over_their_inputs(mla):
+    """An output row may be its own input row, at the same addresses and strides; every other overlap would be read half
+    written."""
+    d = dims(mla)
+    at = lambda i: FAKE + (i << 24)
+    ok = dict(dims=ctypes.byref(d), kv=at(0), kv_stride=288, kv_gamma=at(1), cq=at(2), cq_stride=1600, cq_gamma=at(3),
+              cq_out=at(4), cq_out_stride=1536, eps=1e-6, pos=at(5), slot=at(6), cache=at(7), num_pages=4, T=5, err=None,
+              stream=None)
+    f = mla.lib.mla_append_normed
+    row = 2 * 1600
+    for bad in (dict(cq_out=at(2)),                                        # c_Q's rows with another stride
+                dict(cq_out=at(2) + 16, cq_out_stride=1600), dict(cq_out=at(2) + row, cq_out_stride=1600),
+                dict(cq_out=at(2) - row, cq_out_stride=1600), dict(cq_out=at(2) + 2 * 1535, cq_out_stride=1600),
+                dict(cq_out=at(0)), dict(cq_out=at(0) + 4 * 2 * 288 + 2 * 287), dict(cq_out=at(1)), dict(cq_out=at(3)),
+                dict(cq_out=at(5)), dict(cq_out=at(6)), dict(cq_out=at(7)), dict(cache=at(0)), dict(cache=at(2)),
+                dict(cache=at(4)), dict(cache=at(6)), dict(cache=at(5) - 4 * 64 * 288 * 2 + 16), dict(cache=at(1)),
+                dict(kv=at(2) + 2 * 1500, kv_stride=1600, cq_out=at(2), cq_out_stride=1600)):
+        assert call(f, ok, **bad) == INVALID, bad
+    ok = dict(dims=ctypes.byref(d), q=at(0), q_stride=16 * 160, gamma=at(1), eps=1e-6, pos=at(2), qc=at(3), qc_ts=16 * 128,
+              qc_hs=128, qr=at(4), qr_ts=16 * 32, qr_hs=32, T=2, stream=None)
+    f = mla.lib.mla_query_norm_rope
+    own = dict(q_stride=16 * 160, qc_ts=16 * 160, qc_hs=160, qr_ts=16 * 160, qr_hs=160)
+    for bad in (dict(qc=at(0)), dict(qr=at(0)), dict(qr=at(0) + 2 * 128), dict(qc=at(1)), dict(qr=at(1)), dict(qc=at(2)),
+                dict(qr=at(2)), dict(qr=at(3)), dict(qc=at(4) - 2 * 16 * 128 + 2), {**own, "qc": at(0) + 2},
+                {**own, "qc": at(0), "qr": at(0) + 2 * 126}, {**own, "qc": at(0) + 2 * 160}, {**own, "qr": at(0)},
+                {**own, "qr": at(0) + 2 * (128 + 16 * 160)}, {**own, "qc": at(0) - 2 * 16 * 160}):
+        assert call(f, ok, **bad) == INVALID, bad
