@@ -65,6 +65,12 @@ class Args {
     if (!t.is_cuda() || t.layout() != c10::kStrided || t.get_device() != dev_ || !t.is_contiguous()) throw Bad{};
     return t;
   }
+  // An address as a number.
+  void* address(int i) const {
+    void* p = PyLong_AsVoidPtr(a_[i]);
+    if (!p && PyErr_Occurred()) throw Bad{};
+    return p;
+  }
   int integer(int i) const {
     const long v = PyLong_AsLong(a_[i]);
     if ((v == -1 && PyErr_Occurred()) || v != (int)v) throw Bad{};
@@ -251,9 +257,40 @@ PyObject* attend_ragged(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+PyObject* ragged_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return status([&]() -> long {
+    Args a(args, n, 13);
+    const auto* w = static_cast<const mla_weights*>(a.address(0));
+    mla_dims d{};
+    if (const mla_status s = mla_weights_dims(w, &d)) return s;
+    const auto dt = type_of(d);
+    const auto i32 = at::kInt;
+    const auto& h = a.tensor(2, dt, {kAny, d.d_model});
+    const int64_t T = h.size(0);
+    a.memory(1);  // the weights' buffer, on the tensors' device
+    const auto& kv_len = a.tensor(4, i32, {kAny});
+    const int64_t B = kv_len.size(0);
+    const auto& q_start = a.tensor(3, i32, {B + 1});
+    const auto& seq = a.tensor(5, i32, {T});
+    const auto& pos = a.tensor(6, i32, {T});
+    const auto& table = a.tensor(7, i32, {B, kAny});
+    const int num_pages = a.integer(8);
+    const auto& cache = a.tensor(9, dt, {kAny, d.page_size, row_of(d)});
+    const auto& out = a.tensor(10, at::kFloat, {T, d.n_h, d.d_v});
+    const auto& ws = a.memory(11);
+    const cudaStream_t st = a.stream(12);
+    if (T > INT_MAX || B > INT_MAX || table.size(1) > INT_MAX || num_pages > cache.size(0)) throw Bad{};
+    return unlocked([&] {
+      return mla_ragged_step(w, h.data_ptr(), ptr<int32_t>(q_start), ptr<int32_t>(kv_len), ptr<int32_t>(seq),
+                             ptr<int32_t>(pos), ptr<int32_t>(table), (int)table.size(1), num_pages, cache.data_ptr(),
+                             ptr<float>(out), (int)B, (int)T, ws.data_ptr(), ws.nbytes(), st);
+    });
+  });
+}
+
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(plan_step), ENTRY(append_normed), ENTRY(query_norm_rope), ENTRY(attend_ragged),
-                         {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(ragged_step), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ragged", "Ragged-step calls of libmla on torch tensors.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

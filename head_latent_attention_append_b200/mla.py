@@ -290,21 +290,22 @@ def _path_dtype(dims: Dims):
 
 def _refuse(fn: str, code: int, tensors):
     """Raises for a call that answered `code`.  Each tensor: (name, tensor or None, dtype, shape (None: any size),
-    packed: contiguous, else with a contiguous last axis); the first one gives the device."""
+    packed: contiguous, else with a contiguous last axis); dtype or shape None: any; the first one on a GPU gives the
+    device."""
     import torch
     if code != 1:
         raise MlaError(fn, code)
-    device = None
+    devices = [t.device for _, t, *_ in tensors if isinstance(t, torch.Tensor)]
+    device = next((d for d in devices if d.type == "cuda"), devices[0])
     for name, t, dtype, shape, packed in tensors:
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
             raise MlaError(fn, -1, f"{name}: a tensor is expected")
-        device = t.device if device is None else device
         got = tuple(t.shape)
-        if t.dtype != dtype:
+        if dtype is not None and t.dtype != dtype:
             raise MlaError(fn, -1, f"{name}: {t.dtype}, expected {dtype}")
-        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+        if shape is not None and (len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got))):
             raise MlaError(fn, -1, f"{name}: shape {got}, expected {tuple('any' if w is None else w for w in shape)}")
         if t.device != device:
             raise MlaError(fn, -1, f"{name} is on {t.device}, expected {device}")
@@ -313,6 +314,18 @@ def _refuse(fn: str, code: int, tensors):
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise MlaError(fn, -1, f"tensors are on {device}, expected the current CUDA device")
     raise MlaError(fn, -1, "an argument is missing or of another kind")
+
+
+def _sized(fn: str, code: int, name: str, t, dims: int) -> int:
+    """The first size of the tensor that gives a call its size, where the call answered `code`."""
+    import torch
+    if code != 1:
+        raise MlaError(fn, code)
+    if not isinstance(t, torch.Tensor):
+        raise MlaError(fn, -1, f"{name}: a tensor is expected")
+    if t.dim() != dims:
+        raise MlaError(fn, -1, f"{name}: shape {tuple(t.shape)}, expected {dims} axes")
+    return t.shape[0]
 
 
 def plan_step(new_len, past_len, free_pages, page_table, num_pages: int, q_start, kv_len, seq_idx, pos, slot, counts,
@@ -388,11 +401,23 @@ def ragged_step_workspace_bytes(dims: Dims, B: int, T: int) -> int:
 
 def ragged_step(w: Weights, h, q_start, kv_len, seq_idx, pos, page_table, num_pages: int, cache, out, workspace,
                 stream=None):
-    """Append and attention of every request's new tokens, from hidden states (include/mla.h)."""
-    _check("mla_ragged_step", lib.mla_ragged_step(
-        w.handle, _ptr(h), _ptr(q_start), _ptr(kv_len), _ptr(seq_idx), _ptr(pos), _ptr(page_table), page_table.shape[1],
-        num_pages, _ptr(cache), _ptr(out), kv_len.shape[0], h.shape[0], _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    """Append and attention of every request's new tokens, from hidden states (include/mla.h).  num_pages: at most the
+    cache's."""
+    s = (_ragged or _module()).ragged_step(w.handle.value if w.handle else 0, w.buffer, h, q_start, kv_len, seq_idx, pos,
+                                           page_table, num_pages, cache, out, workspace, stream)
+    if s:
+        import torch
+        fn, d, dt, i32 = "mla_ragged_step", w.dims, _path_dtype(w.dims), torch.int32
+        T, B = _sized(fn, s, "h", h, 2), _sized(fn, s, "kv_len", kv_len, 1)
+        if isinstance(num_pages, int) and num_pages > _sized(fn, s, "cache", cache, 3):
+            raise MlaError(fn, -1, f"num_pages: {num_pages}, the cache has {cache.shape[0]}")
+        _refuse(fn, s, (
+            ("h", h, dt, (T, d.d_model), True), ("q_start", q_start, i32, (B + 1,), True),
+            ("kv_len", kv_len, i32, (B,), True), ("seq_idx", seq_idx, i32, (T,), True), ("pos", pos, i32, (T,), True),
+            ("page_table", page_table, i32, (B, None), True),
+            ("cache", cache, dt, (None, d.page_size, d.d_c + (d.n_h if d.rope_key_per_head else 1) * d.d_r), True),
+            ("out", out, torch.float32, (T, d.n_h, d.d_v), True), ("weights", w.buffer, None, None, True),
+            ("workspace", workspace, None, None, True)))
 
 
 def selftest_wait_timeout(workspace, limit_us: int, stream=None):

@@ -147,3 +147,77 @@ def test_query_outputs_in_other_parts_of_the_rows_of_q(mla, dtype, T, n_h):
             with pytest.raises(mla.MlaError) as e:
                 mla.query_norm_rope(dims, q, gamma, pos, **{"qc_out": qc, "qr_out": qr, **bad})
             assert e.value.code == -1
+
+
+# ------------------------------------------------------------------ refusals
+def spoilt(t, axes, packed=True):
+    """Tensors that cannot stand for `t` (checked along `axes`); each has at least the memory of `t` behind its address."""
+    yield "type", t.to(torch.float64 if t.dtype == torch.int64 else torch.int64)
+    yield "axes", t[None]
+    yield "axes", t.flatten() if t.dim() > 1 else t[:, None].contiguous()
+    yield "device", t.cpu()
+    for axis in axes:
+        if t.shape[axis] > 1:
+            less = t.narrow(axis, 0, t.shape[axis] - 1)
+            # A contiguous tensor of the smaller shape at the start of as much memory.
+            yield f"shorter axis {axis}", t.flatten()[:less.numel()].view(less.shape)
+        size = list(t.shape)
+        size[axis] += 1
+        yield f"longer axis {axis}", t.new_zeros(size)
+    if t.shape[-1] > 1:
+        yield "strided last axis", torch.stack([t, t], -1)[..., 0]
+    if packed and t.dim() > 1 and t.shape[0] > 1:
+        wide = torch.cat([t, t], 1)
+        yield "rows apart", wide[:, :t.shape[1]]
+
+
+def check_refusals(mla, call, tensors, others=(), loose=()):
+    """`tensors`: name -> (tensor, the axes whose size the call knows); `loose`: names that may have rows apart."""
+    good = {k: t for k, (t, _) in tensors.items()}
+    call(**good)
+    torch.cuda.synchronize()
+    for name, (t, axes) in tensors.items():
+        for what, bad in spoilt(t, axes, name not in loose):
+            with pytest.raises(mla.MlaError) as e:
+                call(**{**good, name: bad})
+            assert e.value.code == -1 and f"({name}" in str(e.value), (name, what, str(e.value))
+    for kw in others:
+        with pytest.raises(mla.MlaError) as e:
+            call(**{**good, **kw})
+        assert e.value.code == -1, kw
+    call(**good)
+    torch.cuda.synchronize()
+
+
+def step_tensors(T, B, pages, width):
+    z = lambda *n, dtype=torch.int32: torch.zeros(n, dtype=dtype, device=DEV)
+    return z, dict(q_start=(i32([0] * B + [T]), (0,)), kv_len=(i32([0] * (B - 1) + [T]), ()),
+                   page_table=(z(B, width) % pages, (0,)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ragged_step_refuses_tensors_that_are_not_the_calls(mla, dtype):
+    from head_latent_attention_append_b200 import synth, workload
+    wl = synth.Workload("ragged", 22, 4, 32, 32, 128, 16, 128, 0, dtype, "decode", 2, 1, 0)
+    weights = mla.Weights(workload.dims_of(wl), workload.upload_weights(wl, synth.make_weights(wl, 5), torch.device(DEV)))
+    T, B, pages = 5, 3, 4
+    z, t = step_tensors(T, B, pages, 2)
+    t.update(h=(z(T, 128, dtype=DT[dtype]), (1,)), seq_idx=(i32([B - 1] * T), (0,)), pos=(i32(range(T)), (0,)),
+             cache=(z(pages, 64, 144, dtype=DT[dtype]), (1, 2)), out=(z(T, 4, 32, dtype=torch.float32), (0, 1, 2)))
+    ws = z(mla.ragged_step_workspace_bytes(weights.dims, B, T), dtype=torch.uint8)
+
+    def call(num_pages=pages, workspace=ws, stream=None, w=weights, **kw):
+        mla.ragged_step(w, kw["h"], kw["q_start"], kw["kv_len"], kw["seq_idx"], kw["pos"], kw["page_table"], num_pages,
+                        kw["cache"], kw["out"], workspace, stream)
+
+    check_refusals(mla, call, t, others=(dict(num_pages=pages + 1), dict(num_pages=0), dict(num_pages=None),
+                                         dict(workspace=None), dict(workspace=ws.cpu()), dict(h=None), dict(out=None)))
+    assert mla.get_error(ws) == 0
+    with pytest.raises(mla.MlaError) as e:
+        call(workspace=ws[:-256].contiguous(), **{k: v for k, (v, _) in t.items()})
+    assert e.value.code == -3
+    call(num_pages=pages - 1, **{k: v for k, (v, _) in t.items()})          # fewer than the cache has: allowed
+    weights.close()
+    with pytest.raises(mla.MlaError) as e:
+        call(**{k: v for k, (v, _) in t.items()})
+    assert e.value.code == -1
