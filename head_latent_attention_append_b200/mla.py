@@ -335,8 +335,9 @@ def plan_step(new_len, past_len, free_pages, page_table, num_pages: int, q_start
                                          pos, slot, counts, device_error, stream)
     if s:
         import torch
-        i32, B, rows = torch.int32, new_len.shape[0], seq_idx.shape[0]
-        _refuse("mla_plan_step", s, (
+        fn, i32 = "mla_plan_step", torch.int32
+        B, rows = _sized(fn, s, "new_len", new_len, 1), _sized(fn, s, "seq_idx", seq_idx, 1)
+        _refuse(fn, s, (
             ("new_len", new_len, i32, (B,), True), ("past_len", past_len, i32, (B,), True),
             ("free_pages", free_pages, i32, (None,), True), ("page_table", page_table, i32, (B, None), True),
             ("q_start", q_start, i32, (B + 1,), True), ("kv_len", kv_len, i32, (B,), True),
@@ -352,10 +353,11 @@ def append_normed(dims: Dims, kv, kv_gamma, pos, slot, cache, eps: float = 1e-6,
                                              device_error, stream)
     if s:
         import torch
-        dt, T, row = _path_dtype(dims), kv.shape[0], dims.d_c + (dims.n_h if dims.rope_key_per_head else 1) * dims.d_r
+        fn, dt = "mla_append_normed", _path_dtype(dims)
+        T, row = _sized(fn, s, "kv", kv, 2), dims.d_c + (dims.n_h if dims.rope_key_per_head else 1) * dims.d_r
         if (cq is None) != (cq_out is None):
-            raise MlaError("mla_append_normed", -1, "cq and cq_out go together")
-        _refuse("mla_append_normed", s, (
+            raise MlaError(fn, -1, "cq and cq_out go together")
+        _refuse(fn, s, (
             ("kv", kv, dt, (T, row), False), ("kv_gamma", kv_gamma, dt, (dims.d_c,), True),
             ("pos", pos, torch.int32, (T,), True), ("slot", slot, torch.int64, (T,), True),
             ("cache", cache, dt, (None, dims.page_size, row), True), ("cq", cq, dt, (T, dims.d_cq), False),
@@ -368,10 +370,11 @@ def query_norm_rope(dims: Dims, q, gamma, pos, qc_out, qr_out, eps: float = 1e-6
     s = (_ragged or _module()).query_norm_rope(dims, q, gamma, pos, qc_out, qr_out, eps, stream)
     if s:
         import torch
-        dt, T, n_h, d_h, d_r = _path_dtype(dims), q.shape[0], dims.n_h, dims.d_h, dims.d_r
-        if s == 1 and q.dim() == 3 and n_h > 1 and q.shape[1:] == (n_h, d_h + d_r) and q.stride(1) != d_h + d_r:
-            raise MlaError("mla_query_norm_rope", -1, "q: a token's heads have to be contiguous")
-        _refuse("mla_query_norm_rope", s, (
+        fn, dt, n_h, d_h, d_r = "mla_query_norm_rope", _path_dtype(dims), dims.n_h, dims.d_h, dims.d_r
+        T = _sized(fn, s, "q", q, 3)
+        if n_h > 1 and q.shape[1:] == (n_h, d_h + d_r) and q.stride(1) != d_h + d_r:
+            raise MlaError(fn, -1, "q: a token's heads have to be contiguous")
+        _refuse(fn, s, (
             ("q", q, dt, (T, n_h, d_h + d_r), False), ("gamma", gamma, dt, (d_h,), True),
             ("pos", pos, torch.int32, (T,), True), ("qc_out", qc_out, dt, (T, n_h, d_h), False),
             ("qr_out", qr_out, dt, (T, n_h, d_r), False)))
@@ -386,13 +389,14 @@ def attend_ragged(dims: Dims, q, q_start, kv_len, page_table, cache, out, lse, w
     s = (_ragged or _module()).attend_ragged(dims, q, q_start, kv_len, page_table, cache, out, lse, workspace, stream)
     if s:
         import torch
-        dt, i32, T, B, n_h, row = _path_dtype(dims), torch.int32, q.shape[0], kv_len.shape[0], dims.n_h, dims.d_c + dims.d_r
-        _refuse("mla_attend_ragged", s, (
+        fn, dt, i32, n_h, row = "mla_attend_ragged", _path_dtype(dims), torch.int32, dims.n_h, dims.d_c + dims.d_r
+        T, B = _sized(fn, s, "q", q, 3), _sized(fn, s, "kv_len", kv_len, 1)
+        _refuse(fn, s, (
             ("q", q, dt, (T, n_h, row), False), ("q_start", q_start, i32, (B + 1,), True),
             ("kv_len", kv_len, i32, (B,), True), ("page_table", page_table, i32, (B, None), True),
             ("cache", cache, dt, (None, dims.page_size, row), True), ("out", out, dt, (T, n_h, dims.d_c), True),
             ("lse", lse, torch.float32, (T, n_h), True),
-            ("workspace", workspace, workspace.dtype, tuple(workspace.shape), True)))
+            ("workspace", workspace, None, None, True)))
 
 
 def ragged_step_workspace_bytes(dims: Dims, B: int, T: int) -> int:

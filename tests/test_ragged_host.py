@@ -194,3 +194,38 @@ def test_append_and_query_refuse_outputs_over_their_inputs(mla):
                 {**own, "qc": at(0), "qr": at(0) + 2 * 126}, {**own, "qc": at(0) + 2 * 160}, {**own, "qr": at(0)},
                 {**own, "qr": at(0) + 2 * (128 + 16 * 160)}, {**own, "qc": at(0) - 2 * 16 * 160}):
         assert call(f, ok, **bad) == INVALID, bad
+
+
+def test_arguments_that_are_no_tensors_are_named(mla):
+    """The calls' own error, whichever argument is not a tensor."""
+    d = dims(mla, d_cq=0)
+    t = torch.zeros(2, 3, 4)
+    calls = {
+        "plan_step": (mla.plan_step, ("new_len", "past_len", "free_pages", "page_table", "q_start", "kv_len", "seq_idx", "pos",
+                                      "slot", "counts"), dict(num_pages=4)),
+        "append_normed": (lambda **kw: mla.append_normed(d, **kw), ("kv", "kv_gamma", "pos", "slot", "cache"), {}),
+        "query_norm_rope": (lambda **kw: mla.query_norm_rope(d, **kw), ("q", "gamma", "pos", "qc_out", "qr_out"), {}),
+        "attend_ragged": (lambda **kw: mla.attend_ragged(d, **kw), ("q", "q_start", "kv_len", "page_table", "cache", "out",
+                                                                     "lse", "workspace"), {}),
+    }
+    for fn, (call_, names, more) in calls.items():
+        for name in names:
+            for bad in (None, [1, 2], 3, "x", t[0, 0, 0]):
+                with pytest.raises(mla.MlaError) as e:
+                    call_(**{**dict.fromkeys(names, t), **more, name: bad})
+                assert e.value.code == INVALID and fn in str(e.value), (fn, name, bad)
+        # The argument that gives the call its size.
+        for bad in (None, [1, 2], 3):
+            with pytest.raises(mla.MlaError, match=rf"\({names[0]}: a tensor is expected"):
+                call_(**{**dict.fromkeys(names, t), **more, names[0]: bad})
+
+
+def test_a_workspace_that_is_missing_is_refused(mla):
+    """Everything else as the call wants it, on the CPU."""
+    d = dims(mla, d_cq=0)
+    bf, i32 = torch.bfloat16, torch.int32
+    with pytest.raises(mla.MlaError) as e:
+        mla.attend_ragged(d, torch.zeros(5, 16, 288, dtype=bf), torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32),
+                          torch.zeros(2, 4, dtype=i32), torch.zeros(3, 64, 288, dtype=bf), torch.zeros(5, 16, 256, dtype=bf),
+                          None, None)
+    assert e.value.code == INVALID
