@@ -66,11 +66,7 @@ class Args {
     return t;
   }
   // An address as a number.
-  void* address(int i) const {
-    void* p = PyLong_AsVoidPtr(a_[i]);
-    if (!p && PyErr_Occurred()) throw Bad{};
-    return p;
-  }
+  void* address(int i) const { return as_address(a_[i]); }
   int integer(int i) const {
     const long v = PyLong_AsLong(a_[i]);
     if ((v == -1 && PyErr_Occurred()) || v != (int)v) throw Bad{};
@@ -94,15 +90,21 @@ class Args {
   // None: torch's current stream; a raw handle; or an object with one.
   cudaStream_t stream(int i) const {
     if (none(i)) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev_).stream();
-    if (PyLong_Check(a_[i])) return reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(a_[i]));
+    if (PyLong_Check(a_[i])) return static_cast<cudaStream_t>(as_address(a_[i]));
     PyObject* h = PyObject_GetAttrString(a_[i], "cuda_stream");
     if (!h) throw Bad{};
     void* p = PyLong_AsVoidPtr(h);
     Py_DECREF(h);
-    return reinterpret_cast<cudaStream_t>(p);
+    if (!p && PyErr_Occurred()) throw Bad{};  // null is a stream, the legacy one
+    return static_cast<cudaStream_t>(p);
   }
 
  private:
+  static void* as_address(PyObject* o) {
+    void* p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw Bad{};
+    return p;
+  }
   PyObject* const* a_;
   int64_t dev_ = -1;
 };

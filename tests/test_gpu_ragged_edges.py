@@ -221,3 +221,26 @@ def test_ragged_step_refuses_tensors_that_are_not_the_calls(mla, dtype):
     with pytest.raises(mla.MlaError) as e:
         call(**{k: v for k, (v, _) in t.items()})
     assert e.value.code == -1
+
+
+def test_a_stream_that_is_none_is_refused(mla):
+    """Not run on the legacy stream, which is what a failed conversion to an address gives."""
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    t = dict(q=torch.ones(1, 1, 48, device=DEV), gamma=None, pos=i32([0]))
+    dims = dims_of(mla, "f32", 1, 32, 64, 16)
+    qc, qr = torch.zeros(1, 1, 32, device=DEV), torch.zeros(1, 1, 16, device=DEV)
+    for bad in ("0", 0.5, 2 ** 70, Stream("0"), Stream(None), Stream(2 ** 70), object()):
+        with pytest.raises(mla.MlaError) as e:
+            mla.query_norm_rope(dims, **t, qc_out=qc, qr_out=qr, stream=bad)
+        assert e.value.code == -1
+        torch.cuda.synchronize()
+        assert not qc.any() and not qr.any()
+    for good in (None, 0, torch.cuda.current_stream(), torch.cuda.Stream(), Stream(0)):
+        qc.zero_()
+        torch.cuda.synchronize()
+        mla.query_norm_rope(dims, **t, qc_out=qc, qr_out=qr, stream=good)
+        torch.cuda.synchronize()
+        assert (qc == 1).all()
