@@ -195,6 +195,77 @@ def step_tensors(T, B, pages, width):
                    page_table=(z(B, width) % pages, (0,)))
 
 
+@pytest.mark.parametrize("rows", [5, 1])
+def test_plan_refuses_tensors_that_are_not_the_calls(mla, rows):
+    B = 3
+    z = lambda *n, dtype=torch.int32: torch.zeros(n, dtype=dtype, device=DEV)
+    t = dict(new_len=(z(B), ()), past_len=(z(B), (0,)), free_pages=(z(4), ()), page_table=(z(B, 2), (0,)),
+             q_start=(z(B + 1), (0,)), kv_len=(z(B), (0,)), seq_idx=(z(rows), ()), pos=(z(rows), (0,)),
+             slot=(z(rows, dtype=torch.int64), (0,)), counts=(z(3), (0,)), device_error=(z(1), (0,)))
+
+    def call(num_pages=8, stream=None, **kw):
+        mla.plan_step(num_pages=num_pages, stream=stream, **kw)
+
+    check_refusals(mla, call, t, others=(dict(num_pages=0), dict(num_pages=2 ** 40), dict(num_pages="8"), dict(slot=None),
+                                         dict(counts=None), dict(new_len=t["kv_len"][0], past_len=t["kv_len"][0])))
+    call(**{k: v for k, (v, _) in t.items() if k != "device_error"})
+
+
+@pytest.mark.parametrize("dtype,per_head", [("bf16", 0), ("f32", 0), ("bf16", 1)])
+def test_append_refuses_tensors_that_are_not_the_calls(mla, dtype, per_head):
+    T, n_h, d_c, d_r, d_cq = 5, 3, 128, 16, 24
+    dims = dims_of(mla, dtype, n_h, 32, d_c, d_r, d_cq, rope_key_per_head=per_head)
+    row = d_c + (n_h if per_head else 1) * d_r
+    z = lambda *n, dtype=DT[dtype]: torch.zeros(n, dtype=dtype, device=DEV)
+    t = dict(kv=(z(T, row), (1,)), kv_gamma=(z(d_c), (0,)), pos=(z(T, dtype=torch.int32), (0,)),
+             slot=(z(T, dtype=torch.int64) - 1, (0,)), cache=(z(2, 64, row), (1, 2)), cq=(z(T, d_cq), (0, 1)),
+             cq_gamma=(z(d_cq), (0,)), cq_out=(z(T, d_cq), (0, 1)), device_error=(z(1, dtype=torch.int32), (0,)))
+
+    def call(eps=1e-6, stream=None, **kw):
+        mla.append_normed(dims, eps=eps, stream=stream, **kw)
+
+    check_refusals(mla, call, t, loose=("kv", "cq", "cq_out"),
+                   others=(dict(cq=None), dict(cq_out=None), dict(cq=None, cq_out=None), dict(eps="x"), dict(eps=-1.0),
+                           dict(slot=None), dict(cache=None), dict(pos=None)))
+    call(**{**{k: v for k, (v, _) in t.items() if "cq" not in k}, "kv_gamma": None})
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_query_refuses_tensors_that_are_not_the_calls(mla, dtype):
+    T, n_h, d_h, d_r = 5, 3, 32, 16
+    dims = dims_of(mla, dtype, n_h, d_h, 128, d_r)
+    z = lambda *n, dtype=DT[dtype]: torch.zeros(n, dtype=dtype, device=DEV)
+    t = dict(q=(z(T, n_h, d_h + d_r), (1, 2)), gamma=(z(d_h), (0,)), pos=(z(T, dtype=torch.int32), (0,)),
+             qc_out=(z(T, n_h, d_h), (0, 1, 2)), qr_out=(z(T, n_h, d_r), (0, 1, 2)))
+
+    def call(eps=1e-6, stream=None, **kw):
+        mla.query_norm_rope(dims, eps=eps, stream=stream, **kw)
+
+    apart = torch.zeros(T, n_h, d_h + d_r + 8, dtype=DT[dtype], device=DEV)[..., :d_h + d_r]
+    check_refusals(mla, call, t, loose=("q", "qc_out", "qr_out"),
+                   others=(dict(q=apart), dict(pos=None), dict(qc_out=None), dict(qr_out=None), dict(eps=None)))
+    call(**{**{k: v for k, (v, _) in t.items()}, "gamma": None})
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_refuses_tensors_that_are_not_the_calls(mla, dtype):
+    T, B, pages, n_h, d_c, d_r = 5, 3, 4, 3, 128, 16
+    dims = dims_of(mla, dtype, n_h, 32, d_c, d_r)
+    z, t = step_tensors(T, B, pages, 2)
+    t.update(q=(z(T, n_h, d_c + d_r, dtype=DT[dtype]), (1, 2)), cache=(z(pages, 64, d_c + d_r, dtype=DT[dtype]), (1, 2)),
+             out=(z(T, n_h, d_c, dtype=DT[dtype]), (0, 1, 2)), lse=(z(T, n_h, dtype=torch.float32), (0, 1)))
+    ws = z(mla.attend_ragged_workspace_bytes(dims, B, T), dtype=torch.uint8)
+
+    def call(workspace=ws, stream=None, **kw):
+        mla.attend_ragged(dims, workspace=workspace, stream=stream, **kw)
+
+    check_refusals(mla, call, t, loose=("q",),
+                   others=(dict(workspace=None), dict(workspace=ws.cpu()), dict(workspace=ws[::2]), dict(out=None),
+                           dict(cache=None), dict(kv_len=None)))
+    call(**{**{k: v for k, (v, _) in t.items()}, "lse": None})
+    assert mla.get_error(ws) == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_ragged_step_refuses_tensors_that_are_not_the_calls(mla, dtype):
     from head_latent_attention_append_b200 import synth, workload
