@@ -315,3 +315,100 @@ def test_a_stream_that_is_none_is_refused(mla):
         mla.query_norm_rope(dims, **t, qc_out=qc, qr_out=qr, stream=good)
         torch.cuda.synchronize()
         assert (qc == 1).all()
+
+
+# ---------------------------------------------------------------- ragged step
+def small_model(mla, dtype, seed=31):
+    from head_latent_attention_append_b200 import synth, workload
+    wl = synth.Workload("ragged", seed, 8, 64, 64, 128, 32, 256, 64, dtype, "decode", 2, 1, 0)
+    return mla.Weights(workload.dims_of(wl), workload.upload_weights(wl, synth.make_weights(wl, 5), torch.device(DEV)))
+
+
+class Serving:
+    """Plan and step of up to B requests on buffers of `rows` rows."""
+
+    def __init__(self, mla, w, B, rows, num_pages, width, seed):
+        d, dt = w.dims, DT["bf16" if w.dims.dtype == mla.BF16 else "f32"]
+        self.mla, self.w, self.num_pages = mla, w, num_pages
+        self.new, self.past, self.free = i32([0] * B), i32([0] * B), torch.randperm(num_pages, generator=gen(seed), device=DEV).int()
+        self.table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+        self.q_start, self.kv_len, self.counts = i32([0] * (B + 1)), i32([0] * B), i32([0] * 3)
+        self.seq, self.pos = i32([0] * rows), i32([0] * rows)
+        self.slot = torch.zeros(rows, dtype=torch.int64, device=DEV)
+        self.h = randn(gen(seed + 1), rows, d.d_model, dtype=dt)
+        self.cache = torch.full((num_pages, 64, d.d_c + d.d_r), float("nan"), dtype=dt, device=DEV)
+        self.out = torch.zeros(rows, d.n_h, d.d_v, device=DEV)
+        self.ws = torch.empty(mla.ragged_step_workspace_bytes(d, B, rows), dtype=torch.uint8, device=DEV)
+
+    def step(self):
+        self.mla.plan_step(self.new, self.past, self.free, self.table, self.num_pages, self.q_start, self.kv_len, self.seq,
+                           self.pos, self.slot, self.counts)
+        self.mla.ragged_step(self.w, self.h, self.q_start, self.kv_len, self.seq, self.pos, self.table, self.num_pages,
+                             self.cache, self.out, self.ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ragged_step_in_a_graph_on_another_stream(mla, dtype):
+    """Captured with the plan, replayed with other lengths: bit for bit what the calls give one by one."""
+    s = Serving(mla, small_model(mla, dtype), B=4, rows=150, num_pages=12, width=4, seed=3)
+    s.new.copy_(i32([1, 2, 3, 4]))
+    s.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        s.step()
+    for lens in ([1, 2, 3, 4], [150, 0, 0, 0], [64, 65, 1, 20], [0, 0, 0, 0], [0, 1, 0, 0], [100, 60, 0, 1]):
+        got = []
+        for go in (graph.replay, s.step):
+            s.new.copy_(i32(lens))
+            s.table.fill_(-1)
+            s.cache.fill_(float("nan"))
+            s.out.fill_(7)
+            go()
+            used = int(s.counts[1])
+            assert mla.get_error(s.ws) == 0
+            got.append((used, s.out[:used].clone(), s.cache.clone(), s.table.clone()))
+        used = got[0][0]
+        assert used == (100 if lens[:2] == [100, 60] else sum(lens)) == got[1][0]
+        assert torch.equal(got[0][1], got[1][1]) and torch.isfinite(got[0][1]).all() and torch.equal(got[0][3], got[1][3])
+        assert torch.equal(got[0][2].nan_to_num(9.0), got[1][2].nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ragged_steps_on_two_streams_at_once(mla, dtype):
+    w = small_model(mla, dtype)
+    sides = [Serving(mla, w, B=3, rows=90, num_pages=9, width=3, seed=5), Serving(mla, w, B=40, rows=64, num_pages=50, width=2, seed=6)]
+    sides[0].new.copy_(i32([70, 1, 12]))
+    sides[1].new.copy_(i32([1] * 39 + [20]))
+    want = []
+    for s in sides:
+        s.step()
+        want.append(s.out[:int(s.counts[1])].clone())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for s, st in zip(sides, streams):
+            with torch.cuda.stream(st):
+                s.out.fill_(7)
+                s.step()
+        torch.cuda.synchronize()
+        for s, x in zip(sides, want):
+            assert torch.equal(s.out[:x.shape[0]], x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ragged_step_of_no_token_and_of_a_workspace_for_more(mla, dtype):
+    w = small_model(mla, dtype)
+    big = torch.empty(mla.ragged_step_workspace_bytes(w.dims, 30, 700), dtype=torch.uint8, device=DEV)
+    for B, rows in ((1, 1), (2, 5), (30, 700), (30, 699), (5, 64), (29, 513)):
+        s = Serving(mla, w, B=B, rows=rows, num_pages=60, width=13, seed=B)
+        s.new.copy_(i32([rows - (B - 1)] + [1] * (B - 1)))
+        s.step()
+        want, own = s.out.clone(), s.ws
+        s.ws = big
+        s.step()
+        assert mla.get_error(own) == 0 and mla.get_error(big) == 0 and torch.equal(s.out, want) and torch.isfinite(want).all()
+    s = Serving(mla, w, B=2, rows=0, num_pages=2, width=1, seed=1)
+    s.ws = big
+    s.step()
+    assert s.kv_len.tolist() == [0, 0]
