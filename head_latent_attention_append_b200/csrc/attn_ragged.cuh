@@ -14,22 +14,27 @@
 //     a 16-head model fills them with eight tokens, and any number of heads
 //     works;
 //   - each row has its own last key.  Only the pages behind the first row's
-//     last key (at most 1 + 128 / n_h / 64 of a row block) need a mask, and in those the latent
-//     rows are cleared of what a weight of 0 must not meet: rows behind the
-//     block's last key wholly, infinities and NaNs in rows that only some of
-//     the block's rows see (a row that sees one has a NaN sum already, or a
-//     score of -inf there and with it no weight);
+//     last key need a mask (at most 1 + ceil(d / 64) of a row block whose last
+//     row sees d keys more than its first), and in those the latent rows are
+//     cleared of what a weight of 0 must not meet: rows behind the block's last
+//     key wholly, infinities and NaNs in rows that only some of the block's
+//     rows see (a row that sees one has a NaN sum already, or a score of -inf
+//     there and with it no weight);
 //   - the softmax scale is applied to the scores in 32 bits (one FMA with the
 //     running maximum), so the queries come as they are;
 //   - a piece of a cut row block leaves its O in 32 bits, column by column, so
 //     that a warp's store is one line without passing through shared memory,
 //     and the merge adds no rounding.  P (bf16, as the MMA reads it) and the
-//     output are the only roundings.
+//     output are the only roundings to fewer than 32 bits; the weights are
+//     taken by the hardware's 2^x (2^-22 relative).  Against 64 bits the outputs
+//     are off by 1.9e-3 to 2.1e-3 (2-norm), where rounding the exact output once
+//     gives 1.7e-3.
 //
 // Bound by the tensor pipe's page loop (1480 cycles a page, 1244 of them MMAs)
 // and, run back to back, by power: 862 tokens of 128 heads over up to 16,001
-// keys take 2.41 ms, 1190 TFLOP/s, 0.86 of the sustained bf16 rate; a batch of
-// 330 tokens over up to 4171 keys 227 us at full clock.  A change of query rows
+// keys take 2.47 ms, 1160 TFLOP/s, 0.84 of the sustained bf16 rate; a batch of
+// 330 tokens over up to 4171 keys 271 us (234 in short runs, near full clock),
+// 0.69 of it.  A change of query rows
 // costs 12,000 cycles (the next rows' load, this block's output), which the
 // schedule counts.  The page loop sits at the register limit: merging pieces
 // here, calling its ends out of line or handing registers over made it 10 to 20%

@@ -12,15 +12,17 @@
 //   O += P V has 8 rows x 4 NC columns (4 lane + 128 c) in a lane's registers.
 // A 16-byte shared-memory load of a warp costs four cycles whatever it shares,
 // so a tile of R x C values per lane is bound by FMAs only where R C >= 4 (R +
-// C): 8 x 4 here (4 x 2 with 256 threads, or 2 x 2 with 512, were three and
-// four times above it and took 1.5 times as long), 8 x 4 NC in P V.  FMAs are
+// C).  The scores' 8 x 4 is short of that by 1.5 and bound by shared memory (4 x
+// 2 with 256 threads, or 2 x 2 with 512, are short by three and four and took
+// 1.5 times as long); P V's 8 x 4 NC meets it from NC = 2 on.  FMAs are
 // issued in pairs, which took 4% (d_c 512) to 9% (one tile per CTA) off.  A small
 // batch is one tile per CTA and bound by latency, so all rows of a tile are
 // copied asynchronously at once, the next 32 keys while these are worked on
 // (where two buffers fit: rows of up to 432 values).  One bulk copy per row
 // instead of sixteen bytes per thread: 5% faster at d_c 256 in large batches,
 // 5% slower at 512 (registers), 1% slower in small ones.  400 tokens of 16 heads
-// over up to 4000 keys run at 36 TFLOP/s; 39 tokens over up to 517 keys in 32 us.
+// over up to 4000 keys run at 36 of 74 TFLOP/s; 39 tokens over up to 517 keys in
+// 32 us, where 4.4 is their FMAs at that rate.
 #pragma once
 #include "ragged_sched.cuh"
 

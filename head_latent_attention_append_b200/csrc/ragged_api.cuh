@@ -11,7 +11,8 @@ constexpr int kRaggedPairs = 80, kRaggedCtas = 160;
 // load and this block's output, about 6 us against 0.8 us a tile of a wide row
 // on the tensor cores; small against a tile on the CUDA cores.  Measured on
 // batches of 64 to 330 row blocks: with d_c = 512, 3, 6, 9 and 12 tiles gave 249,
-// 238, 232 and 234 us; with d_c = 256, 35.0, 33.5, 35.1 and 36.5.
+// 238, 232 and 234 us; with d_c = 256, 35.0, 33.5, 35.1 and 36.5.  The widths 128
+// and 384 take the line through these two points; they were not measured.
 int block_tiles(const mla_dims& d) { return d.dtype == MLA_BF16 ? 3 + 3 * d.d_c / 256 : 1; }
 
 struct RaggedPlan {

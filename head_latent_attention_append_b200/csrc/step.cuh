@@ -28,7 +28,7 @@ namespace step {
 // (a few microseconds up to thousands of requests, from L2) instead of one
 // kernel making them and a second one waiting for it; then each CTA writes
 // its share of requests, new pages and rows, each row finding its request by
-// a binary search in shared memory.  3.1 us for 64 requests of one token, 4.2
+// a binary search in shared memory.  3.2 us for 64 requests of one token, 4.3
 // for 1024 requests and 21,600 rows (device time; the launch takes the host 3).
 constexpr int PLAN_THREADS = 512;
 constexpr int PLAN_MAX_B = 16384;  // the two sums of every request sit in shared memory
@@ -273,7 +273,8 @@ struct Rope {
 
 // Cosine and sine of pair i's angle at `pos`.  The turns are formed and
 // reduced to [-1/2, 1/2] in 64 bits (a far position makes tens of thousands
-// of them), and the sine and cosine of the reduced angle taken in 32.
+// of them), and the sine and cosine of the reduced angle taken in 32, which
+// leaves rotated values off by 5e-8 of their pair's length (2-norm).
 __device__ __forceinline__ float2 rope_cs(const Rope& r, int pos, int i) {
   const double t = (double)pos * r.turns[i];
   float s, c;
@@ -419,9 +420,10 @@ __device__ __forceinline__ void put_pair(T* p, float2 v) {
 // row.  Each element is read and written once: bound by memory, by latency at
 // decode sizes.  So a warp walks several rows where there are many, keeps its
 // share of gamma, and asks for the next row before it works on this one.
-// 16,384 rows of 2112 bf16 values: 30.3 us, 4.6 TB/s, 0.70 of the measured copy
+// 16,384 rows of 2112 bf16 values: 31.3 us, 4.4 TB/s, 0.68 of the measured copy
 // rate (a block per row without walking 32.9, two rows ahead 38, eight vectors
-// per lane and a warp for all of c_Q 77); 64 rows: 2.5 us.
+// per lane and a warp for all of c_Q 77); neither memory nor issue is full then:
+// a warp has one row on its way and waits at each row's sums.  64 rows: 2.4 us.
 struct NormAppendArgs {
   const void* kv;        // [T][kv_stride]: [c (d_c) | k_R]
   const void* kv_gamma;  // [d_c] or null
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(NORM_THREADS, NV == 2 ? 8 : 4) norm_append_ker
 // share of gamma.  Every element is read and written once.  What bounded the
 // first versions was occupancy (two blocks an SM, 226 us for 4096 tokens of 128
 // heads), then issued instructions (divisions by the group's size, one value
-// at a time, 87 us); now memory: 73 us, 5.5 TB/s, 0.84 of the measured copy rate.
+// at a time, 87 us); now memory: 74.5 us, 5.4 TB/s, 0.82 of the measured copy rate.
 struct QueryArgs {
   const void* q;       // [T][n_h] rows [q_C (d_h) | q_R (d_r)], q_stride per token
   const void* gamma;   // [d_h] or null

@@ -398,9 +398,12 @@ mla_status mla_query_norm_rope(const mla_dims* dims, const void* q, int64_t q_st
  * they are.  Cache rows that no query sees may hold anything.  q_start that
  * decreases or leaves [0, T] computes nothing; a length outside
  * [0, max_pages*64] counts as the nearest one, and the outputs of a request with
- * a page id outside [0, num_pages) are unspecified; a batch of more than 2^31 - 1
- * (128 rows x 64 keys) tiles computes nothing; each sets MLA_ERR_DEVICE_BOUNDS
- * in the workspace error word.  A NaN or infinity in a key that a query does not
+ * a page id outside [0, num_pages) are unspecified; a batch too large for the
+ * schedule computes nothing (it takes the rows in blocks of 128 in bf16, of 64 in
+ * fp32, each of one request, and counts ceil(keys / 64) tiles, at least one, and
+ * 3 + 3 d_c / 256 more in bf16, 1 in fp32, for a block; they may add up to 2^31 -
+ * 1); each sets MLA_ERR_DEVICE_BOUNDS in the workspace error word.  T = 0 does
+ * nothing and leaves that word as it is.  A NaN or infinity in a key that a query does not
  * see does not reach it; one that it does see makes its row NaN, but for an
  * infinity that brings the key's score to -inf, which may count as weight 0.
  * Deterministic.  One shared RoPE key, B <= 16384 and T * n_h < 2^31 - 128 (else
