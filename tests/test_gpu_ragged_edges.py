@@ -412,3 +412,56 @@ def test_ragged_step_of_no_token_and_of_a_workspace_for_more(mla, dtype):
     s.ws = big
     s.step()
     assert s.kv_len.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("dtype,n_h,d_c,d_r", [("bf16", 16, 256, 32), ("bf16", 128, 128, 64), ("f32", 8, 64, 16), ("f32", 5, 61, 6)])
+def test_steps_one_behind_the_other_on_the_same_buffers(mla, dtype, n_h, d_c, d_r):
+    """Each kernel of a step starts while the one before it ends and reads what that one has written, into buffers that
+    the step before read: three steps in one graph, against the same calls with the GPU waited for after each."""
+    B, rows, num_pages, width, d_h = 6, 120, 40, 6, 32
+    dims, dt, g = dims_of(mla, dtype, n_h, d_h, d_c, d_r), DT[dtype], gen(8)
+    plans = [([40, 1, 30, 2, 0, 17], [0] * 6), ([1, 1, 1, 70, 5, 3], [40, 1, 30, 2, 0, 17]),
+             ([3, 64, 1, 1, 1, 40], [41, 2, 31, 72, 5, 20])]
+    plans = [(i32(n), i32(p)) for n, p in plans]
+    free = torch.randperm(num_pages, generator=g, device=DEV).int().view(4, 10)
+    kv, q = [randn(g, rows, d_c + d_r, dtype=dt) for _ in plans], [randn(g, rows, n_h, d_h + d_r, dtype=dt) for _ in plans]
+    gk, gq = randn(g, d_c, dtype=dt), randn(g, d_h, dtype=dt)
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    q_start, kv_len, seq, pos = i32([0] * (B + 1)), i32([0] * B), i32([0] * rows), i32([0] * rows)
+    slot, counts = torch.zeros(rows, dtype=torch.int64, device=DEV), i32([0] * 3)
+    cache = torch.zeros(num_pages, 64, d_c + d_r, dtype=dt, device=DEV)
+    absorbed, qc = randn(g, rows, n_h, d_c + d_r, dtype=dt), torch.empty(rows, n_h, d_h, dtype=dt, device=DEV)
+    outs = [torch.zeros(rows, n_h, d_c, dtype=dt, device=DEV) for _ in plans]
+    lses = [torch.zeros(rows, n_h, device=DEV) for _ in plans]
+    ws = torch.empty(mla.attend_ragged_workspace_bytes(dims, B, rows), dtype=torch.uint8, device=DEV)
+
+    def steps(after=lambda: None):
+        for i, (new, past) in enumerate(plans):
+            mla.plan_step(new, past, free[i], table, num_pages, q_start, kv_len, seq, pos, slot, counts)
+            after()
+            mla.append_normed(dims, kv[i], gk, pos, slot, cache)
+            after()
+            mla.query_norm_rope(dims, q[i], gq, pos, qc, absorbed[..., d_c:])
+            after()
+            mla.attend_ragged(dims, absorbed, q_start, kv_len, table, cache, outs[i], lses[i], ws)
+            after()
+
+    def begin():
+        table.fill_(-1)
+        cache.zero_()
+        for t in outs + lses:
+            t.fill_(7)
+        torch.cuda.synchronize()
+
+    begin()
+    steps(torch.cuda.synchronize)
+    want = [t.clone() for t in outs + lses + [cache, table]]
+    assert mla.get_error(ws) == 0 and all(torch.isfinite(t.float()).all() for t in want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps()
+    for go in [graph.replay, steps] * 10:
+        begin()
+        go()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs + lses + [cache, table], want))
